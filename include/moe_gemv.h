@@ -398,6 +398,134 @@ moe_status moe_layer_forward_noalloc(const moe_weights* w, const float* w_router
                                      int y_dtype, void* stream);
 
 /*
+ * ---- Row operators around the experts -------------------------------------
+ *
+ * The layer's input norm with its gradient, token rows copied into expert
+ * order and combined back with their gradients, and the int8 product: the
+ * steps next to moe_dispatch and the experts for a caller that trains
+ * through them or runs products of its own on the dispatched rows.  They
+ * share the conventions above, with these limits: m and N multiples of 8, m
+ * <= 16384 for the norms, K a multiple of 16, outputs overlapping no input.
+ * Sums and statistics are fp32 (int32 in the product); each output is rounded
+ * once.  No result depends on the timing of workgroups.
+ */
+
+/*
+ * moe_norm_forward -- the layer's input norm as an operator of its own (the
+ * norm of moe_layer_forward_fused), keeping what its gradient needs:
+ *   y[t] = (x[t] - mean[t]) * rstd[t] * gamma + beta    (MOE_NORM_LAYER)
+ *   y[t] = x[t] * rstd[t] * gamma                       (MOE_NORM_RMS)
+ * mean over the m columns; rstd = 1 / sqrt(mean of the squares of what
+ * multiplies it + eps).
+ *  x, y       device [T][m] in dtype (MOE_F32 or MOE_BF16).
+ *  gamma      device fp32 [m].  beta  device fp32 [m] or NULL (layer norm only).
+ *  mean       device fp32 [T] output or NULL (layer norm only).
+ *  rstd       device fp32 [T] output or NULL.
+ *  eps        in [0, 1].
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+moe_status moe_norm_forward(const void* x, int dtype, int norm, const float* gamma, const float* beta, float eps, int T,
+                            int m, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * moe_norm_backward -- the gradients of moe_norm_forward.  With h = (x -
+ * mean) * rstd (mean 0 for the RMS norm) and u = gamma * dy:
+ *   dx     = rstd * (u - h * avg(u * h) - [layer norm] avg(u))   (avg over a row)
+ *   dgamma = sum_t dy[t] * h[t],   dbeta = sum_t dy[t]
+ *  dy, x, dx  device [T][m] in dtype.  gamma  device fp32 [m].
+ *  mean       device fp32 [T], as moe_norm_forward left it (layer norm; NULL for RMS).
+ *  rstd       device fp32 [T], as moe_norm_forward left it.
+ *  dx         may be NULL.  dgamma, dbeta  device fp32 [m], each may be NULL (dbeta:
+ *             layer norm only); they are overwritten, with zeros when T is 0.
+ *  workspace  with dgamma or dbeta: device, 256-byte aligned, at least
+ *             moe_norm_backward_workspace_size(T, m) bytes, one per call in
+ *             flight.  Else NULL.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.
+ */
+moe_status moe_norm_backward_workspace_size(int T, int m, size_t* bytes);
+moe_status moe_norm_backward(const void* dy, const void* x, int dtype, int norm, const float* gamma, const float* mean,
+                             const float* rstd, int T, int m, void* dx, float* dgamma, float* dbeta, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/*
+ * moe_permute_rows -- each token's row copied to its assignments' rows, in
+ * expert order with moe_dispatch's inv_perm:
+ *   x_perm[inv_perm[t*k + j]] = x[t]   for j < k
+ * moe_permute_rows_backward -- its gradient:
+ *   dx[t] = sum_{j<k} dx_perm[inv_perm[t*k + j]]
+ *  inv_perm   device int32 [T*k].  An entry outside [0, rows) is an assignment
+ *             without a row (dropped, as by a capacity limit): it is neither
+ *             written nor read and adds nothing.  Entries inside must differ
+ *             (else which of the equal ones is written is open).
+ *  x, dx      device [T][m].   x_perm, dx_perm  device [rows][m]; rows that no
+ *             entry names are left as they were.
+ *  dtype, row_dtype, x_dtype   MOE_F32 or MOE_BF16, of x and x_perm, of dx_perm, of dx.
+ *  k          1 <= k <= 64.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+moe_status moe_permute_rows(const void* x, int dtype, const int32_t* inv_perm, int T, int m, int k, int rows, void* x_perm,
+                            void* stream);
+moe_status moe_permute_rows_backward(const void* dx_perm, int row_dtype, const int32_t* inv_perm, int T, int m, int k,
+                                     int rows, void* dx, int x_dtype, void* stream);
+
+/*
+ * moe_combine_rows -- moe_combine for expert rows of either type and with
+ * dropped assignments (inv_perm and rows as in moe_permute_rows):
+ *   y[t] = sum_{j<k} topk_w[t][j] * y_perm[inv_perm[t*k + j]]   (fp32 sum, in order of j)
+ * A token without any row gets zeros; a dropped assignment's weight is not used.
+ * moe_combine_rows_backward -- its gradients:
+ *   dy_perm[inv_perm[t*k + j]] = topk_w[t][j] * dy[t]
+ *   d_topk_w[t][j] = sum_i dy[t][i] * y_perm[inv_perm[t*k + j]][i]   (0 for a dropped one)
+ *  y_perm, dy_perm  device [rows][m] in row_dtype; y device [T][m] in y_dtype, dy in
+ *                   dy_dtype (MOE_F32 or MOE_BF16 each).
+ *  topk_w, d_topk_w device fp32 [T][k].
+ *  dy_perm, d_topk_w  one of them may be NULL (without d_topk_w, y_perm may be NULL too).
+ *                   Rows of dy_perm that no entry of inv_perm names are left as they were.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+moe_status moe_combine_rows(const void* y_perm, int row_dtype, const int32_t* inv_perm, const float* topk_w, int T, int m,
+                            int k, int rows, void* y, int y_dtype, void* stream);
+moe_status moe_combine_rows_backward(const void* dy, int dy_dtype, const void* y_perm, int row_dtype,
+                                     const int32_t* inv_perm, const float* topk_w, int T, int m, int k, int rows,
+                                     void* dy_perm, float* d_topk_w, void* stream);
+
+/*
+ * moe_quantize_codes_i8 -- moe_quantize_rows_i8 giving the int8 codes
+ * themselves, the form moe_matmul_i8 takes:
+ *   scale[t] = 2^X, X the smallest integer with max_i |x[t][i]| <= 127 * 2^X;
+ *   codes[t][i] = round-half-even(x[t][i] / scale[t])
+ *  x  device bf16 [T][m] (finite values), m a multiple of 64, 16-byte aligned;
+ *  codes  device int8 [T][m], 16-byte aligned;  scale  device fp32 [T].
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+moe_status moe_quantize_codes_i8(const void* x, int T, int m, int8_t* codes, float* scale, void* stream);
+
+/*
+ * moe_matmul_i8 -- int8 x int8 product with one scale per token and one per
+ * output channel (the INT8 GeMM with both operands quantised of the
+ * DeepSpeed-Inference summary, datalearner.com, section 4), dense or over the
+ * experts' row ranges of a dispatch:
+ *   y[r][n] = x_scale[t] * w_scale[e][n] * sum_{i<K} x[t][i] * w[e][n][i]
+ * for every row r of expert e (offsets[e] <= r < offsets[e+1]), t = perm[r] / topk
+ * (so x stays in token order) or t = r without perm.  The sum is exact in int32.
+ *  x          device int8 [T][K].       x_scale  device fp32 [T].
+ *  w          device int8 [E][N][K]: each output channel's K codes together
+ *             (w1 and w2 of moe_weights_create are [E][K][N]).
+ *  w_scale    device fp32 [E][N].
+ *  offsets    device int32 [E+1] from moe_dispatch, or NULL: E must be 1 and all rows
+ *             are its.  Values are read as if clamped to [0, rows]; rows of no range
+ *             are left as they were.
+ *  perm       device int32 [rows] from moe_dispatch, or NULL (T must equal rows).
+ *             perm[r] / topk is read as if clamped to [0, T).
+ *  y          device [rows][N] in y_dtype (MOE_F32 or MOE_BF16).
+ *  K <= 131056; 1 <= E <= 64; x, w, w_scale and y 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+moe_status moe_matmul_i8(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
+                         const int32_t* offsets, const int32_t* perm, int T, int topk, int rows, int K, int N, int E,
+                         void* y, int y_dtype, void* stream);
+
+/*
  * Measurement aid (not part of the layer).  Between moe_profile_begin and
  * moe_profile_end every kernel the library launches is bracketed by HIP
  * events on its own stream.  moe_profile_end waits for the last event and
@@ -405,7 +533,9 @@ moe_status moe_layer_forward_noalloc(const moe_weights* w, const float* w_router
  * moe_profile_query(name, &total_ms, &launches).  Process-global, not
  * thread-safe; max_launches bounds the events recorded (later launches are
  * not timed).  Kernel names: "route_topk", "dispatch", "ffn_up", "ffn_down",
- * "ffn_f32_up", "ffn_f32_down", "combine", "finalize", "fill".
+ * "ffn_f32_up", "ffn_f32_down", "combine", "finalize", "fill"; of the row
+ * operators "norm_fwd", "norm_bwd", "permute_rows", "permute_rows_bwd",
+ * "combine_rows", "combine_rows_bwd", "quant_rows", "matmul_i8".
  */
 moe_status moe_profile_begin(int max_launches);
 moe_status moe_profile_end(void);

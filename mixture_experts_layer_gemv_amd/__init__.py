@@ -76,6 +76,15 @@ _SIGS = {
     "moe_combine": ([_vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
     "moe_quantize_rows_e4m3": ([_vp, _i32, _i32, _vp, _vp, _vp], _i32),
     "moe_quantize_rows_i8": ([_vp, _i32, _i32, _vp, _vp, _vp], _i32),
+    "moe_norm_forward": ([_vp, _i32, _i32, _vp, _vp, ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
+    "moe_norm_backward_workspace_size": ([_i32, _i32, ctypes.POINTER(_sz)], _i32),
+    "moe_norm_backward": ([_vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "moe_permute_rows": ([_vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp], _i32),
+    "moe_permute_rows_backward": ([_vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
+    "moe_combine_rows": ([_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
+    "moe_combine_rows_backward": ([_vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp], _i32),
+    "moe_quantize_codes_i8": ([_vp, _i32, _i32, _vp, _vp, _vp], _i32),
+    "moe_matmul_i8": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
     "moe_layer_forward": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _sz,
                            _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "moe_layer_forward_fused": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _i32,
@@ -215,6 +224,98 @@ def moe_quantize_rows_e4m3(x, T, m, xq, scale, stream=None):
 
 def moe_quantize_rows_i8(x, T, m, xq, scale, stream=None):
     _check("moe_quantize_rows_i8", lib().moe_quantize_rows_i8(_p(x), T, m, _p(xq), _p(scale), _s(stream)))
+
+
+def _tensors(fn, *sized):
+    """The row operators' tensor arguments as device pointers, each given with
+    the bytes the call reads or writes there; a tensor that is not on the
+    current GPU, not contiguous or too small raises before the call."""
+    out, dev = [], None
+    for t, nbytes in sized:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if dev is None:
+            import torch
+
+            dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        if not t.is_cuda or t.get_device() != dev or not t.is_contiguous() or t.nbytes < nbytes:
+            raise MoeError(fn, MOE_ERR_INVALID_ARG, f"tensor {tuple(t.shape)} on {t.device}: need {nbytes} contiguous "
+                           "bytes on the current GPU")
+        out.append(t.data_ptr())
+    return out
+
+
+def _size(dtype):
+    """Bytes of an element of a value dtype (others are refused by the call)."""
+    return 2 if dtype == MOE_BF16 else 4
+
+
+def moe_norm_forward(x, dtype, norm, gamma, beta, eps, T, m, y, mean=None, rstd=None, stream=None):
+    n = T * m * _size(dtype)
+    x, gamma, beta, y, mean, rstd = _tensors("moe_norm_forward", (x, n), (gamma, 4 * m), (beta, 4 * m), (y, n),
+                                             (mean, 4 * T), (rstd, 4 * T))
+    _check("moe_norm_forward", lib().moe_norm_forward(x, dtype, norm, gamma, beta, eps, T, m, y, mean, rstd,
+                                                      _s(stream)))
+
+
+def moe_norm_backward_workspace_size(T, m) -> int:
+    n = _sz()
+    _check("moe_norm_backward_workspace_size", lib().moe_norm_backward_workspace_size(T, m, ctypes.byref(n)))
+    return n.value
+
+
+def moe_norm_backward(dy, x, dtype, norm, gamma, mean, rstd, T, m, dx, dgamma, dbeta, workspace=None, ws_bytes=0,
+                      stream=None):
+    n = T * m * _size(dtype)
+    dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace = _tensors(
+        "moe_norm_backward", (dy, n), (x, n), (gamma, 4 * m), (mean, 4 * T), (rstd, 4 * T), (dx, n), (dgamma, 4 * m),
+        (dbeta, 4 * m), (workspace, ws_bytes))
+    _check("moe_norm_backward", lib().moe_norm_backward(dy, x, dtype, norm, gamma, mean, rstd, T, m, dx, dgamma, dbeta,
+                                                        workspace, ws_bytes, _s(stream)))
+
+
+def moe_permute_rows(x, dtype, inv_perm, T, m, k, rows, x_perm, stream=None):
+    e = m * _size(dtype)
+    x, inv_perm, x_perm = _tensors("moe_permute_rows", (x, T * e), (inv_perm, 4 * T * k), (x_perm, rows * e))
+    _check("moe_permute_rows", lib().moe_permute_rows(x, dtype, inv_perm, T, m, k, rows, x_perm, _s(stream)))
+
+
+def moe_permute_rows_backward(dx_perm, row_dtype, inv_perm, T, m, k, rows, dx, x_dtype, stream=None):
+    dx_perm, inv_perm, dx = _tensors("moe_permute_rows_backward", (dx_perm, rows * m * _size(row_dtype)),
+                                     (inv_perm, 4 * T * k), (dx, T * m * _size(x_dtype)))
+    _check("moe_permute_rows_backward", lib().moe_permute_rows_backward(dx_perm, row_dtype, inv_perm, T, m, k, rows,
+                                                                        dx, x_dtype, _s(stream)))
+
+
+def moe_combine_rows(y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, y, y_dtype, stream=None):
+    y_perm, inv_perm, topk_w, y = _tensors("moe_combine_rows", (y_perm, rows * m * _size(row_dtype)),
+                                           (inv_perm, 4 * T * k), (topk_w, 4 * T * k), (y, T * m * _size(y_dtype)))
+    _check("moe_combine_rows", lib().moe_combine_rows(y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, y, y_dtype,
+                                                      _s(stream)))
+
+
+def moe_combine_rows_backward(dy, dy_dtype, y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, dy_perm, d_topk_w,
+                              stream=None):
+    r = rows * m * _size(row_dtype)
+    dy, y_perm, inv_perm, topk_w, dy_perm, d_topk_w = _tensors(
+        "moe_combine_rows_backward", (dy, T * m * _size(dy_dtype)), (y_perm, r), (inv_perm, 4 * T * k),
+        (topk_w, 4 * T * k), (dy_perm, r), (d_topk_w, 4 * T * k))
+    _check("moe_combine_rows_backward", lib().moe_combine_rows_backward(
+        dy, dy_dtype, y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, dy_perm, d_topk_w, _s(stream)))
+
+
+def moe_quantize_codes_i8(x, T, m, codes, scale, stream=None):
+    x, codes, scale = _tensors("moe_quantize_codes_i8", (x, 2 * T * m), (codes, T * m), (scale, 4 * T))
+    _check("moe_quantize_codes_i8", lib().moe_quantize_codes_i8(x, T, m, codes, scale, _s(stream)))
+
+
+def moe_matmul_i8(x, x_scale, w, w_scale, offsets, perm, T, topk, rows, K, N, E, y, y_dtype, stream=None):
+    x, x_scale, w, w_scale, offsets, perm, y = _tensors(
+        "moe_matmul_i8", (x, T * K), (x_scale, 4 * T), (w, E * N * K), (w_scale, 4 * E * N), (offsets, 4 * (E + 1)),
+        (perm, 4 * rows), (y, rows * N * _size(y_dtype)))
+    _check("moe_matmul_i8", lib().moe_matmul_i8(x, x_scale, w, w_scale, offsets, perm, T, topk, rows, K, N, E, y,
+                                                y_dtype, _s(stream)))
 
 
 def moe_layer_forward(w, w_router, b_router, x, x_dtype, T, m, p, E, k, y, y_dtype, workspace, ws_bytes,

@@ -17,6 +17,7 @@
 #include "moe_gemv.h"
 #include "moe_index.hpp"
 #include "moe_kernels.hpp"
+#include "moe_rows.hpp"
 
 // The plan inputs of a layer: its shape, dtypes and tuning.  Every launch
 // choice and the workspace layout are functions of this, T and k (and the
@@ -1602,6 +1603,264 @@ moe_status moe_profile_query(const char* kernel, double* total_ms, int* launches
   auto it = g_prof.total.find(kernel);
   *total_ms = it == g_prof.total.end() ? 0.0 : it->second.first;
   *launches = it == g_prof.total.end() ? 0 : it->second.second;
+  return ok();
+}
+
+}  // extern "C"
+
+// ---- row operators around the experts --------------------------------------------
+
+namespace {
+
+moe_status check_rows_shape(int T, int m, int max_m = 0) {
+  if (T < 0 || m <= 0) return fail(MOE_ERR_INVALID_ARG, "bad sizes T=%d m=%d", T, m);
+  if (m % 8) return fail(MOE_ERR_UNSUPPORTED, "m=%d must be a multiple of 8", m);
+  if (max_m && m > max_m) return fail(MOE_ERR_UNSUPPORTED, "m=%d exceeds %d", m, max_m);
+  return MOE_OK;
+}
+
+moe_status check_value_dtype(const char* what, int dtype) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s %d unsupported", what, dtype);
+  return MOE_OK;
+}
+
+moe_status check_norm(int dtype, int norm, int T, int m) {
+  if (norm != MOE_NORM_LAYER && norm != MOE_NORM_RMS) return fail(MOE_ERR_INVALID_ARG, "norm kind %d", norm);
+  if (moe_status rc = check_rows_shape(T, m, moe::kNormMaxCols)) return rc;
+  return check_value_dtype("dtype", dtype);
+}
+
+size_t norm_backward_bytes(int T, int m) {
+  return (size_t)2 * (size_t)moe::norm_backward_blocks(T, m, device_cus()) * (size_t)m * sizeof(float);
+}
+
+// Shapes of the permute and combine operators.
+moe_status check_assignments(int T, int m, int k, int rows) {
+  if (moe_status rc = check_rows_shape(T, m)) return rc;
+  if (k < 1) return fail(MOE_ERR_INVALID_ARG, "k=%d must be >= 1", k);
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
+  if (k > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "k=%d too large", k);
+  if ((long long)T * k > 0x7FFFFFFFLL) return fail(MOE_ERR_UNSUPPORTED, "T*k exceeds 2^31-1");
+  return MOE_OK;
+}
+
+moe_status combine_rows(const char* name, const void* rows_in, int row_dtype, const int32_t* inv, const float* w,
+                        int T, int m, int k, int rows, void* out, int out_dtype, void* stream) {
+  const hipStream_t s = as_stream(stream);
+  moe::RowsArgs a{};
+  a.rows = rows_in;
+  a.inv = inv;
+  a.w = w;
+  a.out = out;
+  a.T = T;
+  a.m = m;
+  a.k = k;
+  a.R = rows;
+  MOE_TRY_HIP(run(name, s, [&] { return moe::launch_combine_rows(a, row_dtype == MOE_BF16, out_dtype == MOE_BF16, s); }));
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_norm_forward(const void* x, int dtype, int norm, const float* gamma, const float* beta, float eps, int T,
+                            int m, void* y, float* mean, float* rstd, void* stream) {
+  if (moe_status rc = check_norm(dtype, norm, T, m)) return rc;
+  if (norm == MOE_NORM_RMS && (beta || mean)) return fail(MOE_ERR_INVALID_ARG, "the RMS norm takes no beta and no mean");
+  if (!(eps >= 0.0f) || eps > 1.0f) return fail(MOE_ERR_INVALID_ARG, "eps=%g must be in [0, 1]", (double)eps);
+  if (T == 0) return ok();
+  if (!x || !gamma || !y) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(x) || !aligned16(y) || !aligned16(gamma) || (beta && !aligned16(beta)))
+    return fail(MOE_ERR_INVALID_ARG, "x, y, gamma and beta must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  moe::NormArgs a{};
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.out = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.eps = eps;
+  a.T = T;
+  a.m = m;
+  MOE_TRY_HIP(run("norm_fwd", s, [&] {
+    return moe::launch_norm_forward(a, dtype == MOE_BF16, norm == MOE_NORM_LAYER, device_cus(), s);
+  }));
+  return ok();
+}
+
+moe_status moe_norm_backward_workspace_size(int T, int m, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  if (moe_status rc = check_rows_shape(T, m, moe::kNormMaxCols)) return rc;
+  *bytes = norm_backward_bytes(T, m);
+  return ok();
+}
+
+moe_status moe_norm_backward(const void* dy, const void* x, int dtype, int norm, const float* gamma, const float* mean,
+                             const float* rstd, int T, int m, void* dx, float* dgamma, float* dbeta, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (moe_status rc = check_norm(dtype, norm, T, m)) return rc;
+  if (norm == MOE_NORM_RMS && (mean || dbeta)) return fail(MOE_ERR_INVALID_ARG, "the RMS norm has no mean and no beta");
+  if (!dx && !dgamma && !dbeta) return fail(MOE_ERR_INVALID_ARG, "no output");
+  if ((dx && !aligned16(dx)) || (dgamma && !aligned16(dgamma)) || (dbeta && !aligned16(dbeta)))
+    return fail(MOE_ERR_INVALID_ARG, "dx, dgamma and dbeta must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  if (T == 0) {  // the sum over no rows
+    for (float* g : {dgamma, dbeta})
+      if (g) MOE_TRY_HIP(run("fill", s, [&] { return moe::launch_fill_zero(g, (size_t)m, s); }));
+    return ok();
+  }
+  if (!dy || !x || !gamma || !rstd || (norm == MOE_NORM_LAYER && !mean)) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(gamma))
+    return fail(MOE_ERR_INVALID_ARG, "dy, x and gamma must be 16-byte aligned");
+  const bool wgrad = dgamma || dbeta;
+  if (wgrad) {
+    const size_t need = norm_backward_bytes(T, m);
+    if (!workspace || ws_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace ? ws_bytes : (size_t)0, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+      return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
+  moe::NormArgs a{};
+  a.x = x;
+  a.dy = dy;
+  a.gamma = gamma;
+  a.out = dx;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.partial = wgrad ? static_cast<float*>(workspace) : nullptr;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.T = T;
+  a.m = m;
+  MOE_TRY_HIP(run("norm_bwd", s, [&] {
+    return moe::launch_norm_backward(a, dtype == MOE_BF16, norm == MOE_NORM_LAYER, device_cus(), s);
+  }));
+  return ok();
+}
+
+moe_status moe_permute_rows(const void* x, int dtype, const int32_t* inv_perm, int T, int m, int k, int rows, void* x_perm,
+                            void* stream) {
+  if (moe_status rc = check_assignments(T, m, k, rows)) return rc;
+  if (moe_status rc = check_value_dtype("dtype", dtype)) return rc;
+  if (T == 0 || rows == 0) return ok();
+  if (!x || !inv_perm || !x_perm) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(x) || !aligned16(x_perm)) return fail(MOE_ERR_INVALID_ARG, "x/x_perm must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  moe::RowsArgs a{};
+  a.tok = x;
+  a.inv = inv_perm;
+  a.out = x_perm;
+  a.T = T;
+  a.m = m;
+  a.k = k;
+  a.R = rows;
+  MOE_TRY_HIP(run("permute_rows", s, [&] { return moe::launch_permute_rows(a, dtype == MOE_BF16, s); }));
+  return ok();
+}
+
+moe_status moe_permute_rows_backward(const void* dx_perm, int row_dtype, const int32_t* inv_perm, int T, int m, int k,
+                                     int rows, void* dx, int x_dtype, void* stream) {
+  if (moe_status rc = check_assignments(T, m, k, rows)) return rc;
+  if (moe_status rc = check_value_dtype("row dtype", row_dtype)) return rc;
+  if (moe_status rc = check_value_dtype("x dtype", x_dtype)) return rc;
+  if (T == 0) return ok();
+  if (!inv_perm || !dx || (rows > 0 && !dx_perm)) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(dx_perm) || !aligned16(dx)) return fail(MOE_ERR_INVALID_ARG, "dx_perm/dx must be 16-byte aligned");
+  return combine_rows("permute_rows_bwd", dx_perm, row_dtype, inv_perm, nullptr, T, m, k, rows, dx, x_dtype, stream);
+}
+
+moe_status moe_combine_rows(const void* y_perm, int row_dtype, const int32_t* inv_perm, const float* topk_w, int T, int m,
+                            int k, int rows, void* y, int y_dtype, void* stream) {
+  if (moe_status rc = check_assignments(T, m, k, rows)) return rc;
+  if (moe_status rc = check_value_dtype("row dtype", row_dtype)) return rc;
+  if (moe_status rc = check_value_dtype("y dtype", y_dtype)) return rc;
+  if (T == 0) return ok();
+  if (!inv_perm || !topk_w || !y || (rows > 0 && !y_perm)) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(y_perm) || !aligned16(y)) return fail(MOE_ERR_INVALID_ARG, "y_perm/y must be 16-byte aligned");
+  return combine_rows("combine_rows", y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, y, y_dtype, stream);
+}
+
+moe_status moe_combine_rows_backward(const void* dy, int dy_dtype, const void* y_perm, int row_dtype,
+                                     const int32_t* inv_perm, const float* topk_w, int T, int m, int k, int rows,
+                                     void* dy_perm, float* d_topk_w, void* stream) {
+  if (moe_status rc = check_assignments(T, m, k, rows)) return rc;
+  if (moe_status rc = check_value_dtype("dy dtype", dy_dtype)) return rc;
+  if (moe_status rc = check_value_dtype("row dtype", row_dtype)) return rc;
+  if (T == 0) return ok();
+  if (!dy_perm && !d_topk_w && rows > 0) return fail(MOE_ERR_INVALID_ARG, "no output");
+  if (!dy || !inv_perm || (dy_perm && !topk_w) || (d_topk_w && rows > 0 && !y_perm))
+    return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(dy) || !aligned16(y_perm) || !aligned16(dy_perm))
+    return fail(MOE_ERR_INVALID_ARG, "dy, y_perm and dy_perm must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  moe::RowsArgs a{};
+  a.tok = dy;
+  a.rows = y_perm;
+  a.inv = inv_perm;
+  a.w = topk_w;
+  a.out = dy_perm;
+  a.dw = d_topk_w;
+  a.T = T;
+  a.m = m;
+  a.k = k;
+  a.R = rows;
+  MOE_TRY_HIP(run("combine_rows_bwd", s, [&] {
+    return moe::launch_combine_rows_backward(a, dy_dtype == MOE_BF16, row_dtype == MOE_BF16, s);
+  }));
+  return ok();
+}
+
+moe_status moe_quantize_codes_i8(const void* x, int T, int m, int8_t* codes, float* scale, void* stream) {
+  if (T < 0 || m <= 0) return fail(MOE_ERR_INVALID_ARG, "bad sizes T=%d m=%d", T, m);
+  if (m % 64) return fail(MOE_ERR_UNSUPPORTED, "m=%d must be a multiple of 64", m);
+  if (T == 0) return ok();
+  if (!x || !codes || !scale) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(x) || !aligned16(codes)) return fail(MOE_ERR_INVALID_ARG, "x/codes must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  MOE_TRY_HIP(run("quant_rows", s, [&] {
+    return moe::launch_quant_rows(static_cast<const uint16_t*>(x), T, m, true, nullptr, reinterpret_cast<uint8_t*>(codes),
+                                  scale, s);
+  }));
+  return ok();
+}
+
+moe_status moe_matmul_i8(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
+                         const int32_t* offsets, const int32_t* perm, int T, int topk, int rows, int K, int N, int E,
+                         void* y, int y_dtype, void* stream) {
+  if (T < 0 || rows < 0 || K <= 0 || N <= 0 || E < 1)
+    return fail(MOE_ERR_INVALID_ARG, "bad sizes T=%d rows=%d K=%d N=%d E=%d", T, rows, K, N, E);
+  if (perm && topk < 1) return fail(MOE_ERR_INVALID_ARG, "topk=%d must be >= 1", topk);
+  if (perm && rows > 0 && T < 1) return fail(MOE_ERR_INVALID_ARG, "rows=%d of no tokens", rows);
+  if (!perm && T != rows) return fail(MOE_ERR_INVALID_ARG, "T=%d must equal rows=%d without perm", T, rows);
+  if (!offsets && E != 1) return fail(MOE_ERR_INVALID_ARG, "E=%d needs offsets", E);
+  if (E > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "E=%d exceeds %d", E, MOE_MAX_EXPERTS);
+  if (K % 16 || N % 8) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 16 and N=%d of 8", K, N);
+  if (K > moe::kI8MaxK) return fail(MOE_ERR_UNSUPPORTED, "K=%d exceeds %d", K, moe::kI8MaxK);
+  if (moe_status rc = check_value_dtype("y dtype", y_dtype)) return rc;
+  if (((long long)rows / 64 + E) * ((N + 15) / 16) >= 1LL << 24)  // a launch holds fewer than 2^32 threads
+    return fail(MOE_ERR_UNSUPPORTED, "rows=%d by N=%d is too large", rows, N);
+  if (rows == 0) return ok();
+  if (!x || !x_scale || !w || !w_scale || !y) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(w_scale) || !aligned16(y))
+    return fail(MOE_ERR_INVALID_ARG, "x, w, w_scale and y must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  moe::I8Args a{};
+  a.x = x;
+  a.sx = x_scale;
+  a.w = w;
+  a.sw = w_scale;
+  a.offsets = offsets;
+  a.perm = perm;
+  a.y = y;
+  a.T = T;
+  a.topk = topk;
+  a.R = rows;
+  a.K = K;
+  a.N = N;
+  a.E = E;
+  MOE_TRY_HIP(run("matmul_i8", s, [&] { return moe::launch_matmul_i8(a, y_dtype == MOE_BF16, device_cus(), s); }));
   return ok();
 }
 

@@ -1,0 +1,187 @@
+"""moe_matmul_i8 and moe_quantize_codes_i8 against the definition in 64 bits.
+
+The int32 sum is exact, so an output differs from the exact value by the
+roundings of its conversion to fp32 (u = 2^-24 relative), of the two scale
+products (u each) and of the store (half a step of the output type).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import mixture_experts_layer_gemv_amd as M
+
+from _gpu import log
+
+pytestmark = pytest.mark.gpu
+
+u = 2.0**-24
+U = {torch.float32: 2.0**-24, torch.bfloat16: 2.0**-8}
+CODE = {torch.float32: M.MOE_F32, torch.bfloat16: M.MOE_BF16}
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    M.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def codes(shape, seed, lo=-127, hi=127):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(lo, hi + 1, shape, generator=g, dtype=torch.int8, device="cuda")
+
+
+def scales(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand(shape, generator=g, device="cuda") + 0.5) * 0.01
+
+
+def exact(x, sx, w, sw, offsets, perm, topk, rows):
+    """y in 64 bits; NaN where no expert has the row."""
+    E, N, _ = w.shape
+    y = torch.full((rows, N), float("nan"), dtype=torch.float64, device="cuda")
+    for e in range(E):
+        lo, hi = (0, rows) if offsets is None else (int(offsets[e]), int(offsets[e + 1]))
+        at = torch.arange(lo, hi, device="cuda")
+        t = at if perm is None else perm.long()[at] // topk
+        if hi > lo:
+            y[lo:hi] = (x[t].double() @ w[e].double().t()) * sx[t].double()[:, None] * sw[e].double()
+    return y
+
+
+def run(x, sx, w, sw, offsets, perm, topk, rows, out):
+    E, N, K = w.shape
+    buf = torch.full((rows * N + 128,), 7.0, dtype=out, device="cuda")
+    y = buf[64:64 + rows * N].view(rows, N)
+    M.moe_matmul_i8(x, sx, w, sw, offsets, perm, len(x), topk, rows, K, N, E, y, CODE[out])
+    torch.cuda.synchronize()
+    assert bool((buf[:64] == 7).all()) and bool((buf[64 + rows * N:] == 7).all())
+    return y
+
+
+def check(y, ref, out, what=""):
+    rows = ~torch.isnan(ref).any(1)
+    assert bool((y[~rows] == 7).all()), "rows of no expert were written"
+    err, r = (y[rows].double() - ref[rows]).abs(), ref[rows].abs()
+    bar = r * (U[out] + 3 * u) * (1 + 2.0**-7) + 1e-37
+    log(f"  {what}: {float((err / bar).max()) if err.numel() else 0:.3f} of the bound")
+    assert bool((err <= bar).all()), what
+
+
+DENSE = [(1, 16, 8), (1, 64, 16), (3, 48, 24), (16, 4096, 512), (17, 80, 40), (64, 256, 1000), (65, 1040, 264),
+         (100, 16, 4104), (128, 512, 256), (200, 2048, 520), (257, 272, 776), (511, 1024, 1032), (1003, 656, 2048),
+         (1500, 144, 4096), (2049, 4096, 1000), (4100, 528, 1288)]
+
+
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,K,N", DENSE)
+def test_dense(R, K, N, out):
+    log(f"matmul_i8 dense R={R} K={K} N={N} {out}")
+    x, w, sx, sw = codes((R, K), R + K), codes((1, N, K), N), scales((R,), 1), scales((1, N), 2)
+    check(run(x, sx, w, sw, None, None, 1, R, out), exact(x, sx, w, sw, None, None, 1, R), out, "y")
+
+
+def grouped(counts, k, seed):
+    """offsets and a perm of a token set of ceil(rows / k) tokens."""
+    g = torch.Generator().manual_seed(seed)
+    rows = sum(counts)
+    offsets = torch.tensor(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32), device="cuda")
+    T = (rows + k - 1) // k
+    perm = torch.randperm(T * k, generator=g)[:rows].to(torch.int32).cuda()
+    return offsets, perm, T, rows
+
+
+COUNTS = {"one_row": [0, 1, 0], "empty_ends": [0, 5, 0, 17, 0], "decode": [4, 1, 0, 7, 2, 16, 9, 1],
+          "hot": [200, 1, 0, 3], "mixed": [64, 65, 63, 128, 1, 0, 15, 16], "large": [300, 257, 1, 512, 700, 0, 255, 31],
+          "e64": [i % 5 for i in range(64)], "even": [256, 256]}
+
+
+@pytest.mark.parametrize("gather", [True, False], ids=["gather", "sorted"])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K,N", [(64, 128), (528, 200), (2048, 768)])
+@pytest.mark.parametrize("counts", COUNTS)
+def test_experts(counts, K, N, out, gather):
+    c = COUNTS[counts]
+    k = 2
+    offsets, perm, T, rows = grouped(c, k, len(c))
+    log(f"matmul_i8 experts {counts} K={K} N={N} {out} gather={gather}")
+    if not gather:
+        perm, T = None, rows
+    x, w, sx, sw = codes((T, K), K), codes((len(c), N, K), N), scales((T,), 1), scales((len(c), N), 2)
+    check(run(x, sx, w, sw, offsets, perm, k, rows, out), exact(x, sx, w, sw, offsets, perm, k, rows), out, "y")
+
+
+@pytest.mark.parametrize("R,N", [(5, 64), (300, 520)])
+def test_extreme_sums(R, N):
+    """Codes of -128 and 127 at the longest K: the largest sums int32 has to hold."""
+    K = 131056
+    x, w = torch.full((R, K), -128, dtype=torch.int8, device="cuda"), torch.full((1, N, K), -128, dtype=torch.int8,
+                                                                               device="cuda")
+    w[:, 1::2] = 127
+    sx, sw = torch.ones(R, device="cuda"), torch.ones(1, N, device="cuda")
+    y = run(x, sx, w, sw, None, None, 1, R, F32)
+    even, odd = 128.0 * 128 * K, -128.0 * 127 * K
+    assert bool((y[:, 0::2].double() - even).abs().max() <= u * even)
+    assert bool((y[:, 1::2].double() - odd).abs().max() <= u * -odd)
+
+
+@pytest.mark.parametrize("R", [6, 400])
+def test_rows_of_no_range_and_clamped_inputs(R):
+    """Rows before the first range, between and behind the ranges stay as they
+    were; offsets and permutation entries outside their range are clamped."""
+    K, N, E = 128, 64, 3
+    x, w, sx, sw = codes((R, K), 1), codes((E, N, K), 2), scales((R,), 3), scales((E, N), 4)
+    offsets = torch.tensor([1, 3, 3, R - 2], dtype=torch.int32, device="cuda")
+    check(run(x, sx, w, sw, offsets, None, 1, R, F32), exact(x, sx, w, sw, offsets, None, 1, R), F32)
+    wild = torch.tensor([-5, 3, 2**31 - 1, R + 7], dtype=torch.int32, device="cuda")  # [0,3) [3,R) [R,R)
+    tame = torch.tensor([0, 3, R, R], dtype=torch.int32, device="cuda")
+    check(run(x, sx, w, sw, wild, None, 1, R, F32), exact(x, sx, w, sw, tame, None, 1, R), F32)
+    perm = torch.arange(R, dtype=torch.int32, device="cuda")
+    perm[0], perm[1], perm[R - 1] = -7, R + 100, 2**31 - 1
+    tame_p = perm.clamp(0, R - 1)
+    check(run(x, sx, w, sw, tame, perm, 1, R, F32), exact(x, sx, w, sw, tame, tame_p, 1, R), F32)
+
+
+def test_same_token_twice():
+    """A token sent to several experts, and twice to one."""
+    K, N = 192, 72
+    x, w, sx, sw = codes((2, K), 1), codes((2, N, K), 2), scales((2,), 3), scales((2, N), 4)
+    perm = torch.tensor([0, 1, 2, 3, 0, 2], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 4, 6], dtype=torch.int32, device="cuda")
+    check(run(x, sx, w, sw, offsets, perm, 2, 6, BF16), exact(x, sx, w, sw, offsets, perm, 2, 6), BF16)
+
+
+def test_offsets_past_32_bits():
+    K, N, E = 8192, 40960, 16  # 5.4 GB of weights
+    w = codes((E, N, K), 5)
+    sw = scales((E, N), 6)
+    c = [0] * (E - 2) + [3, 70]
+    offsets, perm, T, rows = grouped(c, 1, 1)
+    x, sx = codes((T, K), 7), scales((T,), 8)
+    y = run(x, sx, w, sw, offsets, perm, 1, rows, BF16)
+    check(y, exact(x, sx, w, sw, offsets, perm, 1, rows), BF16)
+    del w, y
+    K, N, R = 64, 32768, 70000  # 2.3e9 outputs
+    x, w, sx, sw = codes((R, K), 1), codes((1, N, K), 2), scales((R,), 3), scales((1, N), 4)
+    y = torch.empty(R, N, dtype=BF16, device="cuda")
+    M.moe_matmul_i8(x, sx, w, sw, None, None, R, 1, R, K, N, 1, y, M.MOE_BF16)
+    pick = torch.tensor([0, 1, 65535, 65537, R - 2, R - 1], device="cuda")
+    check(y[pick], exact(x[pick], sx[pick], w, sw, None, None, 1, len(pick)), BF16)
+
+
+def test_quantize_codes():
+    for T, m in [(1, 64), (5, 256), (33, 4096)]:
+        g = torch.Generator().manual_seed(m)
+        x = (torch.randn(T, m, generator=g) * torch.logspace(-20, 20, T)[:, None]).to(BF16).cuda()
+        x[0] = 0
+        c, s = torch.empty(T, m, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+        M.moe_quantize_codes_i8(x, T, m, c, s)
+        v, s2 = torch.empty_like(x), torch.empty_like(s)
+        M.moe_quantize_rows_i8(x, T, m, v, s2)
+        assert torch.equal(s, s2) and torch.equal((c.double() * s.double()[:, None]), v.double())
+        _, codes_o, scales_o = oracle.quant_rows_i8(x.view(torch.int16).cpu().numpy().view(np.uint16))
+        assert np.array_equal(c.cpu().numpy(), codes_o) and np.array_equal(s.cpu().numpy(), scales_o)
