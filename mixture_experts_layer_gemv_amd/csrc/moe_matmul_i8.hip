@@ -9,21 +9,45 @@
 // weights take the product's row side (operand A) and the tokens its column
 // side, so that a lane's accumulators are consecutive output channels of one
 // token.
+#include <type_traits>
+
+#include "moe_index.hpp"
 #include "moe_kernels.hpp"
+#include "moe_lds.hpp"
 #include "moe_rows.hpp"
 
 namespace moe {
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-// The row range of expert e, kept inside [0, R] whatever the offsets hold.
-__device__ __forceinline__ int row_at(const I8Args& A, int e) {
-  if (!A.offsets) return e ? A.R : 0;
-  const int o = A.offsets[e];
-  return o < 0 ? 0 : (o > A.R ? A.R : o);
+// The experts' row offsets into LDS: clamped to [0, R], a decreasing entry
+// counting as its predecessor, so that the ranges are disjoint and in bounds
+// whatever the caller's array holds.
+__device__ __forceinline__ void load_offsets(const I8Args& A, int* offs) {
+  if (threadIdx.x == 0 && !A.offsets) {
+    offs[0] = 0;
+    offs[1] = A.R;
+  }
+  if (A.offsets && threadIdx.x < 64) {  // one wave: entries lane and, for the last lane, 64
+    const int lane = threadIdx.x;
+    int o = lane <= A.E ? A.offsets[lane] : 0;
+    o = o < 0 ? 0 : (o > A.R ? A.R : o);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int p = __shfl_up(o, d, 64);
+      if (lane >= d && p > o) o = p;
+    }
+    if (lane <= A.E) offs[lane] = o;
+    if (lane == 63 && A.E == 64) {
+      const int last = A.offsets[64];
+      offs[64] = last < o ? o : (last > A.R ? A.R : last);
+    }
+  }
+  __syncthreads();
 }
 
 // The x row of output row r, kept inside [0, T).
@@ -33,42 +57,25 @@ __device__ __forceinline__ int token_of(const I8Args& A, int r) {
   return t < 0 ? 0 : (t >= A.T ? A.T - 1 : t);
 }
 
-// Four consecutive channels n .. n + 3 of output row r (N is a multiple of 8).
-template <bool YB>
-__device__ __forceinline__ void store4(const I8Args& A, int e, int r, int t, int n, const i32x4_t& acc) {
-  const float sx = A.sx[t];
-  const float4 sw = *reinterpret_cast<const float4*>(A.sw + (size_t)e * A.N + n);
-  const float o[4] = {(float)acc[0] * sx * sw.x, (float)acc[1] * sx * sw.y, (float)acc[2] * sx * sw.z,
-                      (float)acc[3] * sx * sw.w};
-  const size_t at = (size_t)r * A.N + n;
-  if constexpr (YB) {
-    const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{o[0], o[1]}, bf16x2_t));
-    const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{o[2], o[3]}, bf16x2_t));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + at) = make_uint2(lo, hi);
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(A.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
-  }
+__device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
+// ---- few rows: weights straight from memory into the products -------------------
+//
 // A workgroup owns 16 output channels and up to 16 MT rows of one expert; its
 // waves split the reduction and add their int32 sums in LDS.
 template <int MT, bool YB>
 __global__ __launch_bounds__(256) void k_i8_rows(const I8Args A, int pairs) {
   __shared__ i32x4_t part[4][MT][64];
+  __shared__ int offs[kMaxExperts + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n0 = (int)(blockIdx.x / (unsigned)pairs) * 16;
-  int pair = (int)(blockIdx.x % (unsigned)pairs);
-  int e = 0, row0 = 0, end = 0;
-  for (; e < A.E; ++e) {
-    row0 = row_at(A, e);
-    end = row_at(A, e + 1);
-    const int c = end > row0 ? (end - row0 + 16 * MT - 1) / (16 * MT) : 0;
-    if (pair < c) break;
-    pair -= c;
-  }
-  if (e == A.E) return;
-  row0 += pair * 16 * MT;
-  const int rows = min(16 * MT, end - row0);
+  load_offsets(A, offs);
+  int e, chunk, npairs;
+  if (!skinny_pair(offs, A.E, 16 * MT, (int)(blockIdx.x % (unsigned)pairs), &e, &chunk, &npairs)) return;
+  const int row0 = offs[e] + chunk * 16 * MT;
+  const int rows = min(16 * MT, offs[e + 1] - row0);
 
   const int q = 16 * (lane >> 4);  // the lane's bytes of a 64-byte step
   const int n = min(n0 + (lane & 15), A.N - 1);
@@ -102,8 +109,199 @@ __global__ __launch_bounds__(256) void k_i8_rows(const I8Args A, int pairs) {
   for (int i = wave; i < MT; i += 4) {
     const i32x4_t sum = part[0][i][lane] + part[1][i][lane] + part[2][i][lane] + part[3][i][lane];
     const int r = 16 * i + (lane & 15);
-    if (r < rows && nn < A.N) store4<YB>(A, e, row0 + r, token_of(A, row0 + r), nn, sum);
+    if (r >= rows || nn >= A.N) continue;
+    const float sx = A.sx[token_of(A, row0 + r)];
+    const float4 sw = *reinterpret_cast<const float4*>(A.sw + (size_t)e * A.N + nn);
+    const float o[4] = {(float)sum[0] * sx * sw.x, (float)sum[1] * sx * sw.y, (float)sum[2] * sx * sw.z,
+                        (float)sum[3] * sx * sw.w};
+    const size_t at = (size_t)(row0 + r) * A.N + nn;
+    if constexpr (YB)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + at) = make_uint2(pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(A.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
   }
+}
+
+// ---- many rows: tiles through LDS ------------------------------------------------
+//
+// A workgroup of WT x WC waves computes 32 TB WT rows by 32 CB WC channels of
+// one expert.  A stage is 128 bytes of the reduction: one cache line of every
+// row and channel of the tile, copied into LDS with 16 bytes a lane, eight
+// lines a copy, S stages in a ring.  A line's eight 16-byte chunks are stored
+// at chunk ^ (row & 7), so that the 8 lanes of one LDS cycle, which read the
+// same chunk of 8 successive rows, touch all banks once; the copy makes that
+// order by choosing each lane's source chunk.
+template <int TB, int CB, int WT, int WC, int S>
+struct TileShape {
+  static constexpr int waves = WT * WC;
+  static constexpr int BM = 32 * TB * WT, BN = 32 * CB * WC;
+  static constexpr int XB = BM * 128, WB = BN * 128;  // bytes of a stage
+  static constexpr int CPX = BM / 8 / waves, CPW = BN / 8 / waves, CP = CPX + CPW;  // copies per wave and stage
+  static_assert(BM % (8 * waves) == 0 && BN % (8 * waves) == 0, "every wave issues the same copies");
+  static_assert(CP * (S - 1) <= 63, "vmcnt holds at most 63");
+};
+
+// global -> LDS, 16 bytes a lane from 64-bit addresses (see copy_frag).
+__device__ __forceinline__ void copy_rows(const void* p, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(p), "s"(lds)
+      : "memory");
+}
+
+template <int TB, int CB, int WT, int WC, int S, bool YB>
+__global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg) {
+  using Sh = TileShape<TB, CB, WT, WC, S>;
+  __shared__ __attribute__((aligned(1024))) unsigned char ring[S][Sh::XB + Sh::WB];
+  __shared__ int offs[kMaxExperts + 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wt = wave / WC, wc = wave % WC;
+  load_offsets(A, offs);
+  const int NBL = (A.N + Sh::BN - 1) / Sh::BN;
+  int e, mb, nb;
+  const int L = xcd_item(blockIdx.x, gemm_items(offs, A.E, Sh::BM, NBL), 0);
+  if (L < 0 || !gemm_item(offs, A.E, Sh::BM, NBL, cg, L, &e, &mb, &nb)) return;
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int row0 = __builtin_amdgcn_readfirstlane(offs[e]) + mb * Sh::BM;
+  const int rows = min(Sh::BM, __builtin_amdgcn_readfirstlane(offs[e + 1]) - row0);
+  const int n0 = nb * Sh::BN;
+
+  // copies: lane l of a copy brings chunk (l % 8) ^ (l / 8) of the copy's row
+  // l / 8 (rows past the tile's last and channels past N re-read the last one)
+  const int c16 = 16 * ((lane & 7) ^ (lane >> 3));
+  const int8_t* xsrc[Sh::CPX];
+  uint32_t wsrc[Sh::CPW];
+  const int8_t* const wbase = A.w + ((size_t)e * A.N + n0) * A.K;
+#pragma unroll
+  for (int j = 0; j < Sh::CPX; ++j) {
+    const int r = min(8 * (Sh::CPX * wave + j) + (lane >> 3), rows - 1);
+    xsrc[j] = A.x + (size_t)token_of(A, row0 + r) * A.K;
+  }
+#pragma unroll
+  for (int j = 0; j < Sh::CPW; ++j)
+    wsrc[j] = (uint32_t)min(8 * (Sh::CPW * wave + j) + (lane >> 3), A.N - 1 - n0) * (uint32_t)A.K;
+  const uint32_t lds0 = lds_address(&ring[0][0]);
+  auto issue = [&](int s) {
+    const int k = min(s * 128 + c16, A.K - 16);  // past K: any bytes of the row, multiplied by zeros
+    const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);
+#pragma unroll
+    for (int j = 0; j < Sh::CPX; ++j) copy_rows(xsrc[j] + k, at + (Sh::CPX * wave + j) * 1024);
+#pragma unroll
+    for (int j = 0; j < Sh::CPW; ++j)
+      copy_frag(wbase, wsrc[j] + (uint32_t)k, at + Sh::XB + (Sh::CPW * wave + j) * 1024);
+  };
+
+  i32x16_t acc[CB][TB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[c][i][v] = 0;
+
+  // operand reads: lane l takes chunk 2 ks + l / 32 of row l % 32 of a block
+  const int half = lane >> 5;
+  const int rowoff = (lane & 31) * 128;
+  auto step = [&](int s, int ks, bool tail) {
+    const unsigned char* st = ring[s % S];
+    const int at = rowoff + (((2 * ks + half) ^ (lane & 7)) * 16);
+    i32x4_t xv[TB], wv[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      wv[c] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + c) * 4096 + at);
+      if (tail && s * 128 + 32 * ks + 16 * half >= A.K) wv[c] = i32x4_t{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i) xv[i] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + i) * 4096 + at);
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+        acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[c], xv[i], acc[c][i], 0, 0, 0);
+  };
+
+  const int steps = (A.K + 127) / 128;
+  const int last = steps - 1;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) issue(min(s, last));
+  for (int s = 0; s < last; ++s) {
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
+    ring_barrier();
+    issue(min(s + S - 1, last));
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) step(s, ks, false);
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  ring_barrier();
+  const int kss = (A.K - last * 128 + 31) / 32;
+  for (int ks = 0; ks < kss; ++ks) step(last, ks, true);
+  __syncthreads();  // the ring is free
+
+  // Epilogue: element v of acc[c][i] in lane l is channel 8 (v / 4) + 4 (l /
+  // 32) + v % 4 of channel block c and row l % 32 of row block i.  A wave
+  // stages one row block at a time (32 rows by its 32 CB channels, rows padded
+  // by 16 bytes) and stores it 16 bytes a lane, whole lines of a row together.
+  constexpr int ES = YB ? 2 : 4;
+  constexpr int RB = 32 * CB * ES, STR = RB + 16;  // bytes of a staged row, its stride
+  static_assert(WT * WC * 32 * STR <= S * (Sh::XB + Sh::WB), "the staging fits the ring");
+  unsigned char* const stage = &ring[0][0] + wave * 32 * STR;
+  const int nw = n0 + wc * 32 * CB;  // the wave's first channel
+  float sw[CB][16];
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int n = nw + 32 * c + 8 * g + 4 * half;
+      const float4 f = n < A.N ? *reinterpret_cast<const float4*>(A.sw + (size_t)e * A.N + n) : make_float4(0, 0, 0, 0);
+      sw[c][4 * g] = f.x, sw[c][4 * g + 1] = f.y, sw[c][4 * g + 2] = f.z, sw[c][4 * g + 3] = f.w;
+    }
+#pragma unroll
+  for (int i = 0; i < TB; ++i) {
+    const int rb = (wt * TB + i) * 32;  // the block's first row in the tile
+    if (rb >= rows) break;
+    const int r = min(rb + (lane & 31), rows - 1);
+    const float sx = A.sx[token_of(A, row0 + r)];
+    unsigned char* const mine = stage + (lane & 31) * STR + 4 * half * ES;
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float o[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = (float)acc[c][i][4 * g + v] * sx * sw[c][4 * g + v];
+        unsigned char* const p = mine + (32 * c + 8 * g) * ES;
+        if constexpr (YB)
+          *reinterpret_cast<uint2*>(p) = make_uint2(pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3]));
+        else
+          *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+      }
+    constexpr int LPR = RB / 16;     // lanes per row
+    constexpr int RPI = 64 / LPR;    // rows per store
+#pragma unroll
+    for (int q = 0; q < 32 / RPI; ++q) {
+      const int rr = q * RPI + lane / LPR, col = lane % LPR;
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * STR + col * 16);
+      const int n = nw + col * (16 / ES);
+      if (rb + rr < rows && n < A.N)
+        *reinterpret_cast<uint4*>(static_cast<char*>(A.y) + ((size_t)(row0 + rb + rr) * A.N + n) * ES) = v;
+    }
+  }
+}
+
+template <int TB, int CB, int WT, int WC, int S>
+hipError_t launch_tile(const I8Args& a, bool y_bf16, int cg, hipStream_t s) {
+  using Sh = TileShape<TB, CB, WT, WC, S>;
+  const long long blocks = ((long long)a.R / Sh::BM + (a.R < a.E ? a.R : a.E)) * ((a.N + Sh::BN - 1) / Sh::BN);
+  const unsigned grid = (unsigned)((blocks + 7) / 8 * 8);
+  if (y_bf16) k_i8_tile<TB, CB, WT, WC, S, true><<<grid, WT * WC * 64, 0, s>>>(a, cg);
+  else k_i8_tile<TB, CB, WT, WC, S, false><<<grid, WT * WC * 64, 0, s>>>(a, cg);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -113,6 +311,7 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
   if (a.R <= 0) return hipSuccess;
   if (a.K <= 0 || a.K % 16 || a.K > kI8MaxK || a.N <= 0 || a.N % 8 || a.E < 1 || (!a.offsets && a.E != 1))
     return hipErrorInvalidValue;
+  if (a.R > 64 * a.E) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, 4, s);
   const long long pairs = (long long)a.R / 64 + (a.R < a.E ? a.R : a.E);
   const long long blocks = pairs * ((a.N + 15) / 16);
   if (blocks >= 1LL << 24) return hipErrorInvalidValue;
