@@ -61,54 +61,123 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
-// ---- few rows: weights straight from memory into the products -------------------
+// global -> LDS, 16 bytes a lane from 64-bit addresses (see copy_frag).
+__device__ __forceinline__ void copy_rows(const void* p, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(p), "s"(lds)
+      : "memory");
+}
+
+
+// Upper bound on the row blocks of BM rows.
+long long row_blocks(const I8Args& a, int BM) {
+  return a.offsets ? (long long)a.R / BM + (a.R < a.E ? a.R : a.E) : ((long long)a.R + BM - 1) / BM;
+}
+
+// ---- few rows: every wave streams weights of its own -----------------------------
 //
-// A workgroup owns 16 output channels and up to 16 MT rows of one expert; its
-// waves split the reduction and add their int32 sums in LDS.
-template <int MT, bool YB>
-__global__ __launch_bounds__(256) void k_i8_rows(const I8Args A, int pairs) {
-  __shared__ i32x4_t part[4][MT][64];
+// A workgroup owns 16 CB output channels and up to 16 TB rows of one expert;
+// its W waves split the reduction and add their int32 sums in LDS.  Each wave
+// copies its own lines through a private ring of S stages (128 bytes of every
+// row and channel), so no wave waits for another before the final sum.
+template <int TB, int CB, int W, int S, bool YB>
+__global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
+  constexpr int CPX = 2 * TB, CPW = 2 * CB, CP = CPX + CPW;
+  static_assert(CP * S <= 63, "vmcnt holds at most 63");
+  constexpr int STAGE = CP * 1024;
+  constexpr int RING = W * S * STAGE, PART = W * CB * TB * 1024;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[RING > PART ? RING : PART];
   __shared__ int offs[kMaxExperts + 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n0 = (int)(blockIdx.x / (unsigned)pairs) * 16;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   load_offsets(A, offs);
   int e, chunk, npairs;
-  if (!skinny_pair(offs, A.E, 16 * MT, (int)(blockIdx.x % (unsigned)pairs), &e, &chunk, &npairs)) return;
-  const int row0 = offs[e] + chunk * 16 * MT;
-  const int rows = min(16 * MT, offs[e + 1] - row0);
+  if (!skinny_pair(offs, A.E, 16 * TB, (int)(blockIdx.x / (unsigned)cols), &e, &chunk, &npairs)) return;
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int n0 = (int)(blockIdx.x % (unsigned)cols) * 16 * CB;
+  const int row0 = __builtin_amdgcn_readfirstlane(offs[e] + chunk * 16 * TB);
+  const int rows = min(16 * TB, __builtin_amdgcn_readfirstlane(offs[e + 1]) - row0);
 
-  const int q = 16 * (lane >> 4);  // the lane's bytes of a 64-byte step
-  const int n = min(n0 + (lane & 15), A.N - 1);
-  const int8_t* wrow = A.w + ((size_t)e * A.N + n) * A.K + q;
-  const int8_t* xrow[MT];
+  // copies: lane l brings chunk (l % 8) ^ (l / 8) of row l / 8 of the copy
+  const int c16 = 16 * ((lane & 7) ^ (lane >> 3));
+  const int8_t* xsrc[CPX];
+  uint32_t wsrc[CPW];
+  const int8_t* const wbase = A.w + ((size_t)e * A.N + n0) * A.K;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int r = row0 + min(16 * i + (lane & 15), rows - 1);
-    xrow[i] = A.x + (size_t)token_of(A, r) * A.K + q;
-  }
-  i32x4_t acc[MT] = {};
-  const int steps = (A.K + 63) / 64;
-  const int lo = steps * wave / 4, hi = steps * (wave + 1) / 4;
-  for (int s = lo; s < hi; ++s) {
-    const int k = s * 64;
-    const bool in = k + q < A.K;  // K is a multiple of 16
-    const i32x4_t zero = {0, 0, 0, 0};
-    const i32x4_t wv = in ? *reinterpret_cast<const i32x4_t*>(wrow + k) : zero;
+  for (int j = 0; j < CPX; ++j)
+    xsrc[j] = A.x + (size_t)token_of(A, row0 + min(8 * j + (lane >> 3), rows - 1)) * A.K;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const i32x4_t xv = in ? *reinterpret_cast<const i32x4_t*>(xrow[i] + k) : zero;
-      acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, xv, acc[i], 0, 0, 0);
+  for (int j = 0; j < CPW; ++j) wsrc[j] = (uint32_t)min(8 * j + (lane >> 3), A.N - 1 - n0) * (uint32_t)A.K;
+  unsigned char* const ring = lds + wave * S * STAGE;
+  const uint32_t at0 = lds_address(ring);
+  const int steps = (A.K + 127) / 128;
+  const int lo = (int)((long long)steps * wave / W), hi = (int)((long long)steps * (wave + 1) / W);
+  auto issue = [&](int s, int slot) {
+    const int k = min(min(s, hi - 1) * 128 + c16, A.K - 16);  // past K: any bytes of the row, multiplied by zeros
+    const uint32_t at = at0 + (uint32_t)slot * STAGE;
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) copy_frag(wbase, wsrc[j] + (uint32_t)k, at + (CPX + j) * 1024);
+#pragma unroll
+    for (int j = 0; j < CPX; ++j) copy_rows(xsrc[j] + k, at + j * 1024);
+  };
+  i32x4_t acc[CB][TB] = {};
+  const int rowoff = (lane & 15) * 128, quart = lane >> 4;
+  if (lo < hi) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) issue(lo + s, s);
+    int slot = 0;
+    for (int s = lo; s < hi; ++s) {
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(CP * (S - 1)) : "memory");
+      const unsigned char* st = ring + slot * STAGE;
+      i32x4_t wv[2][CB], xv[2][TB];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int at = rowoff + (((4 * ks + quart) ^ (lane & 7)) * 16);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) wv[ks][c] = *reinterpret_cast<const i32x4_t*>(st + (CPX + 2 * c) * 1024 + at);
+#pragma unroll
+        for (int i = 0; i < TB; ++i) xv[ks][i] = *reinterpret_cast<const i32x4_t*>(st + 2 * i * 1024 + at);
+      }
+      if ((s + 1) * 128 > A.K) {  // the tail: zero weights past K
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+            if (s * 128 + 64 * ks + 16 * quart >= A.K) wv[ks][c] = i32x4_t{0, 0, 0, 0};
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
+      issue(s + S, slot);
+      slot = slot + 1 == S ? 0 : slot + 1;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+          for (int i = 0; i < TB; ++i)
+            acc[c][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[ks][c], xv[ks][i], acc[c][i], 0, 0, 0);
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the last copies have landed: the ring is reused
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
   __syncthreads();
-  // wave i finishes row tile i: a lane holds channels n0 + 4 (lane / 16) .. + 3
+  i32x4_t* const part = reinterpret_cast<i32x4_t*>(lds);  // [W][CB * TB][64]
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int i = 0; i < TB; ++i) part[(wave * CB * TB + c * TB + i) * 64 + lane] = acc[c][i];
+  __syncthreads();
+  // a wave finishes a tile: a lane holds channels 16 c + 4 (lane / 16) .. + 3
   // of row 16 i + lane % 16
-  const int nn = n0 + 4 * (lane >> 4);
-  for (int i = wave; i < MT; i += 4) {
-    const i32x4_t sum = part[0][i][lane] + part[1][i][lane] + part[2][i][lane] + part[3][i][lane];
-    const int r = 16 * i + (lane & 15);
+  for (int f = wave; f < CB * TB; f += W) {
+    const int nn = n0 + 16 * (f / TB) + 4 * (lane >> 4);
+    const int r = 16 * (f % TB) + (lane & 15);
+    i32x4_t sum = part[f * 64 + lane];
+#pragma unroll
+    for (int v = 1; v < W; ++v) sum += part[(v * CB * TB + f) * 64 + lane];
     if (r >= rows || nn >= A.N) continue;
     const float sx = A.sx[token_of(A, row0 + r)];
     const float4 sw = *reinterpret_cast<const float4*>(A.sw + (size_t)e * A.N + nn);
@@ -120,6 +189,16 @@ __global__ __launch_bounds__(256) void k_i8_rows(const I8Args A, int pairs) {
     else
       *reinterpret_cast<float4*>(static_cast<float*>(A.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
   }
+}
+
+template <int TB, int CB, int W, int S>
+hipError_t launch_rows(const I8Args& a, bool y_bf16, hipStream_t s) {
+  const long long cols = (a.N + 16 * CB - 1) / (16 * CB);
+  const long long blocks = row_blocks(a, 16 * TB) * cols;
+  if (blocks * W * 64 >= 1LL << 32) return hipErrorInvalidValue;
+  if (y_bf16) k_i8_rows<TB, CB, W, S, true><<<(unsigned)blocks, W * 64, 0, s>>>(a, (int)cols);
+  else k_i8_rows<TB, CB, W, S, false><<<(unsigned)blocks, W * 64, 0, s>>>(a, (int)cols);
+  return hipGetLastError();
 }
 
 // ---- many rows: tiles through LDS ------------------------------------------------
@@ -141,21 +220,8 @@ struct TileShape {
   static_assert(CP * (S - 1) <= 63, "vmcnt holds at most 63");
 };
 
-// global -> LDS, 16 bytes a lane from 64-bit addresses (see copy_frag).
-__device__ __forceinline__ void copy_rows(const void* p, uint32_t lds) {
-  uint32_t saved;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
-      "global_load_lds_dwordx4 %1, off\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
-      : "v"(p), "s"(lds)
-      : "memory");
-}
-
 template <int TB, int CB, int WT, int WC, int S, bool YB>
-__global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg) {
+__global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg, int rotate) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   __shared__ __attribute__((aligned(1024))) unsigned char ring[S][Sh::XB + Sh::WB];
   __shared__ int offs[kMaxExperts + 1];
@@ -187,8 +253,17 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   for (int j = 0; j < Sh::CPW; ++j)
     wsrc[j] = (uint32_t)min(8 * (Sh::CPW * wave + j) + (lane >> 3), A.N - 1 - n0) * (uint32_t)A.K;
   const uint32_t lds0 = lds_address(&ring[0][0]);
+  const int steps = (A.K + 127) / 128;
+  const int last = steps - 1;
+  // Where a weight tile is read once (rotate), neighbouring column blocks walk
+  // the reduction from different stages: in step with one another they read
+  // the same offset of rows a power of two apart, few of the memory's channels
+  // (474 MB of decode weights: 94 against 86 us).  A partial last stage has to
+  // come last.
+  const int rot = rotate && A.K % 128 == 0 ? nb % steps : 0;
+  auto stage_of = [&](int s) { const int r = s + rot; return r < steps ? r : r - steps; };
   auto issue = [&](int s) {
-    const int k = min(s * 128 + c16, A.K - 16);  // past K: any bytes of the row, multiplied by zeros
+    const int k = min(stage_of(s) * 128 + c16, A.K - 16);  // past K: any bytes of the row, multiplied by zeros
     const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);
 #pragma unroll
     for (int j = 0; j < Sh::CPX; ++j) copy_rows(xsrc[j] + k, at + (Sh::CPX * wave + j) * 1024);
@@ -215,7 +290,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
       wv[c] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + c) * 4096 + at);
-      if (tail && s * 128 + 32 * ks + 16 * half >= A.K) wv[c] = i32x4_t{0, 0, 0, 0};
+      if (tail && stage_of(s) * 128 + 32 * ks + 16 * half >= A.K) wv[c] = i32x4_t{0, 0, 0, 0};
     }
 #pragma unroll
     for (int i = 0; i < TB; ++i) xv[i] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + i) * 4096 + at);
@@ -226,8 +301,6 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
         acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[c], xv[i], acc[c][i], 0, 0, 0);
   };
 
-  const int steps = (A.K + 127) / 128;
-  const int last = steps - 1;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) issue(min(s, last));
   for (int s = 0; s < last; ++s) {
@@ -295,29 +368,34 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
 }
 
 template <int TB, int CB, int WT, int WC, int S>
-hipError_t launch_tile(const I8Args& a, bool y_bf16, int cg, hipStream_t s) {
+hipError_t launch_tile(const I8Args& a, bool y_bf16, int cg, int rot, hipStream_t s) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
-  const long long blocks = ((long long)a.R / Sh::BM + (a.R < a.E ? a.R : a.E)) * ((a.N + Sh::BN - 1) / Sh::BN);
+  const long long blocks = row_blocks(a, Sh::BM) * ((a.N + Sh::BN - 1) / Sh::BN);
+  if ((blocks + 8) * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
   const unsigned grid = (unsigned)((blocks + 7) / 8 * 8);
-  if (y_bf16) k_i8_tile<TB, CB, WT, WC, S, true><<<grid, WT * WC * 64, 0, s>>>(a, cg);
-  else k_i8_tile<TB, CB, WT, WC, S, false><<<grid, WT * WC * 64, 0, s>>>(a, cg);
+  if (y_bf16) k_i8_tile<TB, CB, WT, WC, S, true><<<grid, WT * WC * 64, 0, s>>>(a, cg, rot);
+  else k_i8_tile<TB, CB, WT, WC, S, false><<<grid, WT * WC * 64, 0, s>>>(a, cg, rot);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s) {
-  (void)cus;
   if (a.R <= 0) return hipSuccess;
   if (a.K <= 0 || a.K % 16 || a.K > kI8MaxK || a.N <= 0 || a.N % 8 || a.E < 1 || (!a.offsets && a.E != 1))
     return hipErrorInvalidValue;
-  if (a.R > 64 * a.E) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, 4, s);
-  const long long pairs = (long long)a.R / 64 + (a.R < a.E ? a.R : a.E);
-  const long long blocks = pairs * ((a.N + 15) / 16);
-  if (blocks >= 1LL << 24) return hipErrorInvalidValue;
-  if (y_bf16) k_i8_rows<4, true><<<(unsigned)blocks, 256, 0, s>>>(a, (int)pairs);
-  else k_i8_rows<4, false><<<(unsigned)blocks, 256, 0, s>>>(a, (int)pairs);
-  return hipGetLastError();
+  // The largest tile that still gives three quarters of the CUs an item, for
+  // experts of the mean row count.
+  const long long experts = a.R < a.E ? a.R : a.E, avg = (a.R + experts - 1) / experts, enough = 3 * cus / 4;
+  auto items = [&](int BM, int BN) { return experts * ((avg + BM - 1) / BM) * ((a.N + BN - 1) / BN); };
+  const int cg = 4;  // column blocks that share their rows in an XCD's L2
+  if (avg > 192 && items(256, 256) >= enough) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, 0, s);
+  if (avg > 48 && items(128, 256) >= enough) return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, avg <= 128, s);
+  if (avg > 32 && items(64, 128) >= enough) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, s);
+  if (avg <= 32 && 4 * items(32, 256) >= 5 * cus) return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, 1, s);
+  if ((avg > 16 || a.E > 1) && items(64, 64) >= enough) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, 0, s);
+  if (avg <= 16) return launch_rows<1, 2, 4, 2>(a, y_bf16, s);
+  return launch_rows<2, 2, 8, 1>(a, y_bf16, s);
 }
 
 }  // namespace moe

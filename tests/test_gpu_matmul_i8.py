@@ -85,6 +85,21 @@ def test_dense(R, K, N, out):
     check(run(x, sx, w, sw, None, None, 1, R, out), exact(x, sx, w, sw, None, None, 1, R), out, "y")
 
 
+# wide enough for every tile shape the launch chooses from on 256 CUs: 256 x
+# 256, 128 x 256, 64 x 128, 64 x 64 and 32 x 256 rows by channels, and the two
+# kernels for few rows; K with and without a partial last stage
+WIDE = [(4100, 144, 4104), (3841, 384, 4360), (2049, 272, 4104), (2300, 256, 3080), (515, 208, 4008), (450, 640, 4104),
+        (60, 176, 12296), (64, 256, 12808), (31, 400, 2056), (32, 2064, 136), (16, 4112, 1032), (40, 2064, 72)]
+
+
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,K,N", WIDE)
+def test_dense_tiles(R, K, N, out):
+    log(f"matmul_i8 dense R={R} K={K} N={N} {out}")
+    x, w, sx, sw = codes((R, K), R + K), codes((1, N, K), N), scales((R,), 1), scales((1, N), 2)
+    check(run(x, sx, w, sw, None, None, 1, R, out), exact(x, sx, w, sw, None, None, 1, R), out, "y")
+
+
 def grouped(counts, k, seed):
     """offsets and a perm of a token set of ceil(rows / k) tokens."""
     g = torch.Generator().manual_seed(seed)
@@ -113,6 +128,26 @@ def test_experts(counts, K, N, out, gather):
         perm, T = None, rows
     x, w, sx, sw = codes((T, K), K), codes((len(c), N, K), N), scales((T,), 1), scales((len(c), N), 2)
     check(run(x, sx, w, sw, offsets, perm, k, rows, out), exact(x, sx, w, sw, offsets, perm, k, rows), out, "y")
+
+
+# (counts, K, N): the same for experts
+WIDE_EXPERTS = {"256x256": ([300, 257, 1, 512, 700, 0, 255, 31], 272, 3208), "128x256": ([64, 200, 129, 0, 1, 128, 127, 99], 400, 6280),
+                "64x128": ([40, 65, 64, 0, 33, 90, 1, 47], 256, 3336), "32x256": ([4, 33, 0, 17, 32, 1, 16, 90], 384, 12296),
+                "32x256_tail": ([4, 1, 0, 17, 32, 1, 16, 3], 144, 12808), "64x64": ([4, 33, 0, 17, 32, 1, 16, 90], 528, 2056),
+                "16": ([3, 1, 0, 17, 16, 1, 5, 2], 2064, 200), "32": ([64, 1, 0, 33, 80], 2064, 200)}
+
+
+@pytest.mark.parametrize("gather", [True, False], ids=["gather", "sorted"])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name", WIDE_EXPERTS)
+def test_experts_tiles(name, out, gather):
+    c, K, N = WIDE_EXPERTS[name]
+    offsets, perm, T, rows = grouped(c, 2, len(c))
+    log(f"matmul_i8 experts {name} {out} gather={gather}")
+    if not gather:
+        perm, T = None, rows
+    x, w, sx, sw = codes((T, K), K), codes((len(c), N, K), N), scales((T,), 1), scales((len(c), N), 2)
+    check(run(x, sx, w, sw, offsets, perm, 2, rows, out), exact(x, sx, w, sw, offsets, perm, 2, rows), out, "y")
 
 
 @pytest.mark.parametrize("R,N", [(5, 64), (300, 520)])
