@@ -128,7 +128,8 @@ def _s(stream):
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -230,19 +231,18 @@ def _tensors(fn, *sized):
     """The row operators' tensor arguments as device pointers, each given with
     the bytes the call reads or writes there; a tensor that is not on the
     current GPU, not contiguous or too small raises before the call."""
-    out, dev = [], None
+    out, dev = [], -1
     for t, nbytes in sized:
-        if t is None or isinstance(t, int):
-            out.append(t)
-            continue
-        if dev is None:
-            import torch
+        if t is not None and type(t) is not int:
+            if dev < 0 and t.is_cuda:
+                import torch
 
-            dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-        if not t.is_cuda or t.get_device() != dev or not t.is_contiguous() or t.nbytes < nbytes:
-            raise MoeError(fn, MOE_ERR_INVALID_ARG, f"tensor {tuple(t.shape)} on {t.device}: need {nbytes} contiguous "
-                           "bytes on the current GPU")
-        out.append(t.data_ptr())
+                dev = torch.cuda.current_device()
+            if not t.is_cuda or t.get_device() != dev or t.nbytes < nbytes or not t.is_contiguous():
+                raise MoeError(fn, MOE_ERR_INVALID_ARG, f"tensor {tuple(t.shape)} on {t.device}: need {nbytes} "
+                               "contiguous bytes on the current GPU")
+            t = t.data_ptr()
+        out.append(t)
     return out
 
 
