@@ -11,26 +11,50 @@
 namespace moe {
 namespace {
 
+// (HIP's own uint4 is a struct whose arrays the compiler does not keep in
+// registers once their loads are conditional)
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-// Eight consecutive elements starting at element i (a multiple of 8).
+// Eight consecutive elements starting at element i (a multiple of 8), as
+// loaded; converted only when they are used.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, size_t i, float (&f)[8]) {
-  if constexpr (BF16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Raw8 {
+  u32x4_t v[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    if constexpr (BF16) {
+      v[0] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + i);
+    } else {
+      const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(p) + i);
+      v[0] = q[0];
+      v[1] = q[1];
+    }
+  }
+  __device__ __forceinline__ void clear() {
+    v[0] = u32x4_t{0, 0, 0, 0};
+    if constexpr (!BF16) v[1] = u32x4_t{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      if constexpr (BF16) {
+        f[2 * j] = __uint_as_float(v[0][j] << 16);
+        f[2 * j + 1] = __uint_as_float(v[0][j] & 0xFFFF0000u);
+      } else {
+        f[j] = __uint_as_float(v[0][j]);
+        f[4 + j] = __uint_as_float(v[1][j]);
+      }
     }
-  } else {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* p, size_t i, float (&f)[8]) {
+  Raw8<BF16> r;
+  r.load(p, i);
+  r.get(f);
 }
 
 // Two fp32 -> two bf16, round to nearest even (the hardware conversion).
@@ -41,17 +65,16 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
 template <bool BF16>
 __device__ __forceinline__ void store8(void* p, size_t i, const float (&f)[8]) {
   if constexpr (BF16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-        make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
+    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i) =
+        u32x4_t{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7])};
   } else {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    f32x4_t* q = reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + i);
+    q[0] = f32x4_t{f[0], f[1], f[2], f[3]};
+    q[1] = f32x4_t{f[4], f[5], f[6], f[7]};
   }
 }
 
-// One DPP step of a wave sum: v plus the value that CTRL moves to each lane
-// (0 where none does).
+// v plus the value that the DPP control CTRL moves to each lane (0 where none does).
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_add(float v) {
   return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, ROWS, 0xF, true));
@@ -69,92 +92,132 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 
-// Eight elements as loaded, converted only when they are used.
-template <bool BF16>
-struct Raw8 {
-  uint4 v[BF16 ? 1 : 2];
-  __device__ __forceinline__ void load(const void* p, size_t i) {
-    if constexpr (BF16) {
-      v[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    } else {
-      v[0] = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i)[0];
-      v[1] = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i)[1];
-    }
-  }
-  __device__ __forceinline__ void clear() {
-    v[0] = make_uint4(0, 0, 0, 0);
-    if constexpr (!BF16) v[1] = v[0];
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    if constexpr (BF16) {
-      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-    } else {
-      const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
-    }
-  }
-};
-
-// Adds the waves' values of a team: slot[0 .. waves) in LDS, written before a barrier.
-__device__ __forceinline__ float slot_sum(const float* slot, int waves) {
-  float r = 0.0f;
-  for (int i = 0; i < waves; ++i) r += slot[i];
-  return r;
+// Sum over aligned groups of n = 8, 16 or 32 lanes, the same in each of them:
+// a step adds lanes whose values are equal within the half that they come from.
+__device__ __forceinline__ float group_sum(float v, int n) {
+  v = dpp_add<0xB1, 0xF>(v);   // lane ^ 1
+  v = dpp_add<0x4E, 0xF>(v);   // lane ^ 2
+  v = dpp_add<0x141, 0xF>(v);  // the other half of 8 lanes
+  if (n > 8) v = dpp_add<0x140, 0xF>(v);  // the other half of 16
+  if (n > 16) v += __shfl_xor(v, 16, 64);
+  return v;
 }
 
 // ---- norm -----------------------------------------------------------------------
 //
+// A team of NT threads (8, 16, 32 or a multiple of 64) owns a row; a block
+// holds one or more teams.  A thread keeps V times eight elements: eight
+// together for bf16, twice four for fp32, so that a wave's 16-byte loads and
+// stores always cover whole lines.
+template <bool BF16>
+struct Cols {
+  int lo, hi;  // the first columns of the two fours
+  __device__ __forceinline__ Cols(int tid, int NT, int v)
+      : lo(BF16 ? 8 * (tid + v * NT) : 4 * (tid + 2 * v * NT)), hi(BF16 ? lo + 4 : lo + 4 * NT) {}
+};
+
+template <bool BF16>
+__device__ __forceinline__ void load_raw(u32x4_t (&v)[BF16 ? 1 : 2], const void* p, size_t row, Cols<BF16> c, int m) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+    const int at = i ? c.hi : c.lo;
+    v[i] = u32x4_t{0, 0, 0, 0};
+    if (at < m) v[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + (row + at) * (BF16 ? 2 : 4));
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void from_raw(const u32x4_t (&v)[BF16 ? 1 : 2], float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (BF16) {
+      f[2 * j] = __uint_as_float(v[0][j] << 16);
+      f[2 * j + 1] = __uint_as_float(v[0][j] & 0xFFFF0000u);
+    } else {
+      f[j] = __uint_as_float(v[0][j]);
+      f[4 + j] = __uint_as_float(v[1][j]);
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_row(void* p, size_t row, Cols<BF16> c, int m, const float (&f)[8]) {
+  if constexpr (BF16) {
+    if (c.lo < m) store8<true>(p, row + c.lo, f);
+  } else {
+    if (c.lo < m) *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + c.lo) = f32x4_t{f[0], f[1], f[2], f[3]};
+    if (c.hi < m) *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + c.hi) = f32x4_t{f[4], f[5], f[6], f[7]};
+  }
+}
+
+// The same columns of an fp32 vector (gamma, beta, a row of partial sums); 0 past m.
+template <bool BF16>
+__device__ __forceinline__ void load_vec(const float* p, Cols<BF16> c, int m, float (&f)[8]) {
+  const f32x4_t zero = {0, 0, 0, 0};
+  const f32x4_t a = c.lo < m ? *reinterpret_cast<const f32x4_t*>(p + c.lo) : zero;
+  const f32x4_t b = c.hi < m ? *reinterpret_cast<const f32x4_t*>(p + c.hi) : zero;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[j] = a[j];
+    f[4 + j] = b[j];
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_vec(float* p, Cols<BF16> c, int m, const float (&f)[8]) {
+  if (c.lo < m) *reinterpret_cast<f32x4_t*>(p + c.lo) = f32x4_t{f[0], f[1], f[2], f[3]};
+  if (c.hi < m) *reinterpret_cast<f32x4_t*>(p + c.hi) = f32x4_t{f[4], f[5], f[6], f[7]};
+}
+
+// Sum over a team, the same in all of its threads.  slot is an LDS row of 16
+// per wave of the block; consecutive sums use different rows, so one barrier
+// each is enough: a row is written again only after a barrier that every wave
+// reaches after reading it.
+__device__ __forceinline__ float team_sum(float v, int NT, int first, float* slot) {
+  if (NT < 64) return group_sum(v, NT);
+  v = wave_sum(v);
+  if (NT == 64) return v;
+  const int lane = threadIdx.x & 63, waves = NT >> 6;
+  if (lane == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return group_sum((lane & 15) < waves ? slot[first + (lane & 15)] : 0.0f, 16);
+}
+
 // y = (x - mu) r gamma + beta, mu the row's mean (0 for the RMS norm), r = 1 /
-// sqrt(mean((x - mu)^2) + eps).  One block per row, the row in registers (V
-// vectors of 8 per thread), gamma and beta kept there from row to row; the
-// next row is loaded while this one is summed.
+// sqrt(mean((x - mu)^2) + eps).  gamma and beta stay in registers from row to
+// row; the next row is loaded while this one is summed.
 template <bool BF16, int V, bool LAYER>
-__global__ __launch_bounds__(V == 1 ? 256 : 1024) void k_norm_fwd(const NormArgs A) {
-  // consecutive sums use different rows, so one barrier each is enough: a row
-  // is written again only after a barrier that every wave reaches after reading it
+__global__ __launch_bounds__(V == 1 ? 256 : 1024) void k_norm_fwd(const NormArgs A, int NT) {
   __shared__ float red[2][16];
-  const int tid = threadIdx.x, NT = blockDim.x, wave = tid >> 6, waves = NT >> 6;
-  const int mv = A.m / 8;
-  const float inv_m = 1.0f / (float)A.m;
+  const int team = threadIdx.x / NT, teams = blockDim.x / NT, tid = threadIdx.x - team * NT;
+  const int first = team * NT >> 6;  // the team's first wave
+  const int m = A.m;
+  const float inv_m = 1.0f / (float)m;
   float g[V][8], b[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = tid + v * NT;
+    const Cols<BF16> c(tid, NT, v);
+    load_vec<BF16>(A.gamma, c, m, g[v]);
+    if (LAYER && A.beta) load_vec<BF16>(A.beta, c, m, b[v]);
+    else
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[v][j] = b[v][j] = 0.0f;
-    if (i < mv) {
-      load8<false>(A.gamma, (size_t)i * 8, g[v]);
-      if (LAYER && A.beta) load8<false>(A.beta, (size_t)i * 8, b[v]);
-    }
+      for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
   }
-  Raw8<BF16> next[V];
-  auto fetch = [&](int t) {
+  u32x4_t next[V][BF16 ? 1 : 2];
+  auto fetch = [&](long long t) {
+    if (t >= A.T) t = A.T - 1;  // read, never written
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      next[v].clear();
-      if (tid + v * NT < mv) next[v].load(A.x, (size_t)t * A.m + (size_t)(tid + v * NT) * 8);
-    }
+    for (int v = 0; v < V; ++v) load_raw<BF16>(next[v], A.x, (size_t)t * m, Cols<BF16>(tid, NT, v), m);
   };
-  auto team_sum = [&](float v, float* slot) {
-    v = wave_sum(v);
-    if (waves == 1) return v;
-    if ((tid & 63) == 0) slot[wave] = v;
-    __syncthreads();
-    return slot_sum(slot, waves);
-  };
-  fetch(blockIdx.x);
+  const long long stride = (long long)gridDim.x * teams;
+  fetch((long long)blockIdx.x * teams + team);
   int turn = 0;
-  for (int t = blockIdx.x; t < A.T; t += gridDim.x, turn ^= 1) {
+  for (long long t0 = (long long)blockIdx.x * teams; t0 < A.T; t0 += stride, turn ^= 1) {  // the same count for every team
+    const long long t = t0 + team;
     float f[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) next[v].get(f[v]);
-    if (t + (int)gridDim.x < A.T) fetch(t + gridDim.x);
+    for (int v = 0; v < V; ++v) from_raw<BF16>(next[v], f[v]);
+    if (t0 + stride < A.T) fetch(t + stride);
     float mu = 0.0f;
     if constexpr (LAYER) {
       float s = 0.0f;
@@ -162,34 +225,32 @@ __global__ __launch_bounds__(V == 1 ? 256 : 1024) void k_norm_fwd(const NormArgs
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s += f[v][j];
-      mu = team_sum(s, red[0]) * inv_m;
+      mu = team_sum(s, NT, first, red[0]) * inv_m;
     }
     float q = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool in = tid + v * NT < mv;
+      const Cols<BF16> c(tid, NT, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = in ? f[v][j] - mu : 0.0f;
+        const float d = (j < 4 ? c.lo : c.hi) < m ? f[v][j] - mu : 0.0f;
         f[v][j] = d;
         q = fmaf(d, d, q);
       }
     }
-    const float var = team_sum(q, red[LAYER ? 1 : turn]) * inv_m;
+    const float var = team_sum(q, NT, first, red[LAYER ? 1 : turn]) * inv_m;
     const float r = 1.0f / sqrtf(var + A.eps);
+    if (t >= A.T) continue;
     if (tid == 0) {
       if (LAYER && A.mean) A.mean[t] = mu;
       if (A.rstd) A.rstd[t] = r;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int i = tid + v * NT;
-      if (i < mv) {
-        float o[8];
+      float o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = LAYER ? fmaf(f[v][j] * r, g[v][j], b[v][j]) : f[v][j] * r * g[v][j];
-        store8<BF16>(A.out, (size_t)t * A.m + (size_t)i * 8, o);
-      }
+      for (int j = 0; j < 8; ++j) o[j] = LAYER ? fmaf(f[v][j] * r, g[v][j], b[v][j]) : f[v][j] * r * g[v][j];
+      store_row<BF16>(A.out, (size_t)t * m, Cols<BF16>(tid, NT, v), m, o);
     }
   }
 }
@@ -197,143 +258,147 @@ __global__ __launch_bounds__(V == 1 ? 256 : 1024) void k_norm_fwd(const NormArgs
 // The gradients.  With h = (x - mu) r and u = gamma dy:
 //   dx = r (u - h <u, h> / m - [layer] <u, 1> / m)
 //   dgamma = sum_t dy h,  dbeta = sum_t dy
-// A block holds several teams of NT threads, one row each per step; a thread
-// adds its columns' dy h and dy over the rows its team takes.  The teams' sums
-// are added in LDS, the block writes them as one row of partial sums, and
+// A thread adds its columns' dy h and dy over the rows its team takes.  The
+// block's sums are added in LDS and written as one row of partial sums, and
 // k_norm_wgrad adds those in block order: nothing depends on timing.
-template <bool BF16, int V, bool LAYER, int MAXT>
-__global__ __launch_bounds__(MAXT) __attribute__((amdgpu_waves_per_eu(4))) void k_norm_bwd(const NormArgs A, int NT) {
+template <bool BF16, int V, bool LAYER>
+__global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
   __shared__ float red[4][16];
-  extern __shared__ float acc[];  // gamma [m]; after the rows, with more than one team, [2][m] sums
+  extern __shared__ float acc[];  // [2][m] where the block's sums are added
   const int team = threadIdx.x / NT, teams = blockDim.x / NT, tid = threadIdx.x - team * NT;
-  const int wave = threadIdx.x >> 6, waves = NT >> 6, first = team * waves;  // the team's first wave
-  const int mv = A.m / 8;
-  const float inv_m = 1.0f / (float)A.m;
-  float ag[V][8], ab[V][8];
+  const int first = team * NT >> 6;
+  const int m = A.m;
+  const float inv_m = 1.0f / (float)m;
+  float g[V][8], ag[V][8], ab[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = tid + v * NT;
+    load_vec<BF16>(A.gamma, Cols<BF16>(tid, NT, v), m, g[v]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) ag[v][j] = ab[v][j] = 0.0f;
-    if (i < mv && team == 0) {
-      float f[8];
-      load8<false>(A.gamma, (size_t)i * 8, f);
-      store8<false>(acc, (size_t)i * 8, f);
-    }
   }
-  __syncthreads();
-  Raw8<BF16> nx[V], ny[V];
+  u32x4_t nx[V][BF16 ? 1 : 2], ny[V][BF16 ? 1 : 2];
   float nmu = 0.0f, nr = 0.0f;
-  auto fetch = [&](long long t) {  // rows past the last are zeros
+  auto fetch = [&](long long t) {
+    const long long row = t < A.T ? t : A.T - 1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      nx[v].clear();
-      ny[v].clear();
-      if (t < A.T && tid + v * NT < mv) {
-        nx[v].load(A.x, (size_t)t * A.m + (size_t)(tid + v * NT) * 8);
-        ny[v].load(A.dy, (size_t)t * A.m + (size_t)(tid + v * NT) * 8);
-      }
+      const Cols<BF16> c(tid, NT, v);
+      load_raw<BF16>(nx[v], A.x, (size_t)row * m, c, m);
+      load_raw<BF16>(ny[v], A.dy, (size_t)row * m, c, m);
     }
-    nmu = LAYER && t < A.T ? A.mean[t] : 0.0f;
-    nr = t < A.T ? A.rstd[t] : 0.0f;
+    nmu = LAYER ? A.mean[row] : 0.0f;
+    nr = A.rstd[row];
   };
+  constexpr bool AHEAD = V == 1;  // the next row loaded during this one's sums: with V = 2 there are no registers for it
   const long long stride = (long long)gridDim.x * teams;
-  fetch((long long)blockIdx.x * teams + team);
+  if (AHEAD) fetch((long long)blockIdx.x * teams + team);
   int turn = 0;
   for (long long t0 = (long long)blockIdx.x * teams; t0 < A.T; t0 += stride, turn ^= 2) {  // the same count for every team
     const long long t = t0 + team;
+    const bool live = t < A.T;
+    if (!AHEAD) fetch(t);
     const float mu = nmu, r = nr;
     float h[V][8], u[V][8];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      nx[v].get(h[v]);
-      ny[v].get(u[v]);
+      from_raw<BF16>(nx[v], h[v]);
+      from_raw<BF16>(ny[v], u[v]);
     }
-    if (t0 + stride < A.T) fetch(t + stride);
+    if (AHEAD && t0 + stride < A.T) fetch(t + stride);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool in = tid + v * NT < mv;
-      float g[8];
-      load8<false>(acc, in ? (size_t)(tid + v * NT) * 8 : 0, g);
+      const Cols<BF16> c(tid, NT, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        // outside the row x and dy are 0: h would be -mu r, times 0; kept finite
+        const bool in = live && (j < 4 ? c.lo : c.hi) < m;
         h[v][j] = in ? (h[v][j] - mu) * r : 0.0f;
-        ag[v][j] = fmaf(u[v][j], h[v][j], ag[v][j]);
-        if (LAYER) ab[v][j] += u[v][j];
-        u[v][j] *= g[j];
+        const float d = live ? u[v][j] : 0.0f;
+        ag[v][j] = fmaf(d, h[v][j], ag[v][j]);
+        if (LAYER) ab[v][j] += d;
+        u[v][j] = d * g[v][j];
         s1 = fmaf(u[v][j], h[v][j], s1);
         if (LAYER) s2 += u[v][j];
       }
     }
     if (!A.out) continue;
-    s1 = wave_sum(s1);
-    if (LAYER) s2 = wave_sum(s2);
-    if (waves > 1) {
-      if ((threadIdx.x & 63) == 0) {
-        red[turn][wave] = s1;
-        if (LAYER) red[turn + 1][wave] = s2;
+    // both sums share a barrier
+    float m1, m2 = 0.0f;
+    if (NT < 64) {
+      m1 = group_sum(s1, NT);
+      if (LAYER) m2 = group_sum(s2, NT);
+    } else {
+      m1 = wave_sum(s1);
+      if (LAYER) m2 = wave_sum(s2);
+      if (NT > 64) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = NT >> 6;
+        if (lane == 0) {
+          red[turn][wave] = m1;
+          if (LAYER) red[turn + 1][wave] = m2;
+        }
+        __syncthreads();
+        const bool mine = (lane & 15) < waves;
+        const int at = first + (mine ? lane & 15 : 0);
+        m1 = group_sum(mine ? red[turn][at] : 0.0f, 16);
+        if (LAYER) m2 = group_sum(mine ? red[turn + 1][at] : 0.0f, 16);
       }
-      __syncthreads();
-      s1 = slot_sum(red[turn] + first, waves);
-      if (LAYER) s2 = slot_sum(red[turn + 1] + first, waves);
     }
-    s1 *= inv_m;
-    s2 *= inv_m;
-    if (t >= A.T) continue;
+    m1 *= inv_m;
+    m2 *= inv_m;
+    if (!live) continue;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int i = tid + v * NT;
-      if (i < mv) {
-        float o[8];
+      float o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = (LAYER ? u[v][j] - s2 - h[v][j] * s1 : u[v][j] - h[v][j] * s1) * r;
-        store8<BF16>(A.out, (size_t)t * A.m + (size_t)i * 8, o);
-      }
+      for (int j = 0; j < 8; ++j) o[j] = (LAYER ? u[v][j] - m2 - h[v][j] * m1 : u[v][j] - h[v][j] * m1) * r;
+      store_row<BF16>(A.out, (size_t)t * m, Cols<BF16>(tid, NT, v), m, o);
     }
   }
   if (!A.partial) return;
-  for (int k = 1; k < teams; ++k) {
+  for (int o = NT; o < 64; o <<= 1)  // teams that share a wave
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ag[v][j] += __shfl_xor(ag[v][j], o, 64);
+        if (LAYER) ab[v][j] += __shfl_xor(ab[v][j], o, 64);
+      }
+  const int per = NT < 64 ? 64 : NT, groups = blockDim.x / per, group = threadIdx.x / per;
+  const bool owner = NT >= 64 || (threadIdx.x & 63) < NT;
+  for (int k = 1; k < groups; ++k) {
     __syncthreads();
-    if (team == k) {
+    if (group == k && owner)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int i = tid + v * NT;
-        if (i < mv) {
-          store8<false>(acc, (size_t)i * 8, ag[v]);
-          if (LAYER) store8<false>(acc + A.m, (size_t)i * 8, ab[v]);
-        }
+        const Cols<BF16> c(tid, NT, v);
+        store_vec<BF16>(acc, c, m, ag[v]);
+        if (LAYER) store_vec<BF16>(acc + m, c, m, ab[v]);
       }
-    }
     __syncthreads();
-    if (team == 0) {
+    if (group == 0 && owner)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int i = tid + v * NT;
-        if (i < mv) {
-          float f[8];
-          load8<false>(acc, (size_t)i * 8, f);
+        const Cols<BF16> c(tid, NT, v);
+        float f[8];
+        load_vec<BF16>(acc, c, m, f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ag[v][j] += f[j];
-          if (LAYER) {
-            load8<false>(acc + A.m, (size_t)i * 8, f);
+        for (int j = 0; j < 8; ++j) ag[v][j] += f[j];
+        if (LAYER) {
+          load_vec<BF16>(acc + m, c, m, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ab[v][j] += f[j];
-          }
+          for (int j = 0; j < 8; ++j) ab[v][j] += f[j];
         }
       }
-    }
   }
-  if (team) return;
-  float* const pg = A.partial + (size_t)blockIdx.x * A.m;
-  float* const pb = pg + (size_t)gridDim.x * A.m;
+  if (group || !owner) return;
+  float* const pg = A.partial + (size_t)blockIdx.x * m;
+  float* const pb = pg + (size_t)gridDim.x * m;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = tid + v * NT;
-    if (i < mv) {
-      store8<false>(pg, (size_t)i * 8, ag[v]);
-      if (LAYER) store8<false>(pb, (size_t)i * 8, ab[v]);
-    }
+    const Cols<BF16> c(tid, NT, v);
+    store_vec<BF16>(pg, c, m, ag[v]);
+    if (LAYER) store_vec<BF16>(pb, c, m, ab[v]);
   }
 }
 
@@ -342,30 +407,26 @@ __global__ __launch_bounds__(MAXT) __attribute__((amdgpu_waves_per_eu(4))) void 
 // every 64th row, then add up in LDS.
 __global__ __launch_bounds__(512) void k_norm_wgrad(const float* __restrict__ partial, int blocks, int m,
                                                     float* __restrict__ dgamma, float* __restrict__ dbeta) {
-  __shared__ float4 part[64][8];
+  __shared__ f32x4_t part[64][8];
   float* const out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
   const int q = threadIdx.x & 7, grp = threadIdx.x >> 3;
   const int c = blockIdx.x * 32 + 4 * q;
   const float* p = partial + (size_t)blockIdx.y * blocks * m + c;
-  float4 s = make_float4(0, 0, 0, 0);
+  f32x4_t s = {0, 0, 0, 0};
   if (c < m)
 #pragma unroll 4
-    for (int b = grp; b < blocks; b += 64) {
-      const float4 f = *reinterpret_cast<const float4*>(p + (size_t)b * m);
-      s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
-    }
+    for (int b = grp; b < blocks; b += 64) s += *reinterpret_cast<const f32x4_t*>(p + (size_t)b * m);
   part[grp][q] = s;
 #pragma unroll
   for (int n = 32; n; n >>= 1) {
     __syncthreads();
     if (grp < n) {
-      const float4 f = part[grp + n][q];
-      s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+      s += part[grp + n][q];
       part[grp][q] = s;
     }
   }
-  if (grp == 0 && c < m) *reinterpret_cast<float4*>(out + c) = s;
+  if (grp == 0 && c < m) *reinterpret_cast<f32x4_t*>(out + c) = s;
 }
 
 // ---- rows in expert order ---------------------------------------------------------
@@ -388,15 +449,15 @@ __global__ __launch_bounds__(256) void k_permute_rows(const RowsArgs A, int chun
   for (long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += 4LL * gridDim.x) {
     const int t = (int)(item / slices), c0 = (int)(item % slices) * 64 * kSlice + lane;
     const int mine = token_rows(A, t, lane);
-    const uint4* src = static_cast<const uint4*>(A.tok) + (size_t)t * chunks;
-    uint4 v[kSlice];
+    const u32x4_t* src = static_cast<const u32x4_t*>(A.tok) + (size_t)t * chunks;
+    u32x4_t v[kSlice];
 #pragma unroll
     for (int i = 0; i < kSlice; ++i)
       if (c0 + 64 * i < chunks) v[i] = src[c0 + 64 * i];
     for (int j = 0; j < A.k; ++j) {
       const int r = __builtin_amdgcn_readlane(mine, j);
       if (r < 0) continue;
-      uint4* dst = static_cast<uint4*>(A.out) + (size_t)r * chunks;
+      u32x4_t* dst = static_cast<u32x4_t*>(A.out) + (size_t)r * chunks;
 #pragma unroll
       for (int i = 0; i < kSlice; ++i)
         if (c0 + 64 * i < chunks) dst[c0 + 64 * i] = v[i];
@@ -508,14 +569,16 @@ unsigned wave_grid(long long items) {  // four waves a block, an item each
   return blocks < kMaxGrid ? (unsigned)blocks : (unsigned)kMaxGrid;
 }
 
-// Threads of a team (one row) of the norm kernels, with V vectors per thread.
-int norm_vecs(int m) { return m <= 2048 ? 1 : 2; }
-int norm_threads(int m) {
-  const int per = 8 * norm_vecs(m);
-  return ((m + per - 1) / per + 63) / 64 * 64;
+// Threads of a team for rows of m with V vectors of 8 per thread.
+int norm_threads(int m, int V) {
+  const int n = (m + 8 * V - 1) / (8 * V);
+  return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : (n + 63) / 64 * 64;
 }
-// Teams of a block and blocks per CU of the backward pass.
-int norm_teams(int m) { return norm_threads(m) <= 512 ? 512 / norm_threads(m) : 1; }
+int norm_fwd_vecs(int m) { return m <= 2048 ? 1 : 2; }
+int norm_bwd_vecs(int m) { return m <= 8192 ? 1 : 2; }
+// Teams of a block.
+int norm_fwd_teams(int nt) { return nt <= 256 ? 256 / nt : 1; }
+int norm_bwd_teams(int nt) { return nt <= 512 ? 512 / nt : 1; }
 
 }  // namespace
 
@@ -530,38 +593,38 @@ int norm_teams(int m) { return norm_threads(m) <= 512 ? 512 / norm_threads(m) : 
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
-  const int nt = norm_threads(a.m), most = cus * (2048 / nt);
-  const unsigned grid = (unsigned)(a.T < most ? a.T : most);
+  const int V = norm_fwd_vecs(a.m), nt = norm_threads(a.m, V), teams = norm_fwd_teams(nt), threads = nt * teams;
+  const long long blocks = ((long long)a.T + teams - 1) / teams, most = (long long)cus * (2048 / threads);
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
 #define MOE_FWD1(B, L) k_norm_fwd<B, 1, L>
 #define MOE_FWD2(B, L) k_norm_fwd<B, 2, L>
-  if (norm_vecs(a.m) == 1) MOE_NORM(MOE_FWD1, grid, nt, 0, s>>>(a));
-  else MOE_NORM(MOE_FWD2, grid, nt, 0, s>>>(a));
+  if (V == 1) MOE_NORM(MOE_FWD1, grid, threads, 0, s>>>(a, nt));
+  else MOE_NORM(MOE_FWD2, grid, threads, 0, s>>>(a, nt));
 #undef MOE_FWD1
 #undef MOE_FWD2
   return hipGetLastError();
 }
 
 int norm_backward_blocks(int T, int m, int cus) {
-  const int teams = norm_teams(m), most = 2 * cus;
-  const long long blocks = ((long long)T + teams - 1) / teams;
-  return blocks < most ? (int)blocks : most;
+  const int nt = norm_threads(m, norm_bwd_vecs(m)), teams = norm_bwd_teams(nt);
+  const long long steps = ((long long)T + teams - 1) / teams, most = (long long)cus * (nt <= 512 ? 2 : 1);
+  if (steps <= most) return (int)steps;
+  const long long per = (steps + most - 1) / most;  // the same number of steps for every block but the last
+  return (int)((steps + per - 1) / per);
 }
 
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
+  const int V = norm_bwd_vecs(a.m), nt = norm_threads(a.m, V), threads = nt * norm_bwd_teams(nt);
   const unsigned grid = (unsigned)norm_backward_blocks(a.T, a.m, cus);
-  const int nt = norm_threads(a.m), teams = norm_teams(a.m), threads = nt * teams;
-  const size_t lds = (teams > 1 ? 2 : 1) * sizeof(float) * (size_t)a.m;
-#define MOE_BWD1(B, L) k_norm_bwd<B, 1, L, 512>
-#define MOE_BWD2(B, L) k_norm_bwd<B, 2, L, 512>
-#define MOE_BWD3(B, L) k_norm_bwd<B, 2, L, 1024>
-  if (norm_vecs(a.m) == 1) MOE_NORM(MOE_BWD1, grid, threads, lds, s>>>(a, nt));
-  else if (threads <= 512) MOE_NORM(MOE_BWD2, grid, threads, lds, s>>>(a, nt));
-  else MOE_NORM(MOE_BWD3, grid, threads, lds, s>>>(a, nt));
+  const size_t lds = threads > (nt < 64 ? 64 : nt) ? 2 * sizeof(float) * (size_t)a.m : 0;  // at most 2048 columns
+#define MOE_BWD1(B, L) k_norm_bwd<B, 1, L>
+#define MOE_BWD2(B, L) k_norm_bwd<B, 2, L>
+  if (V == 1) MOE_NORM(MOE_BWD1, grid, threads, lds, s>>>(a, nt));
+  else MOE_NORM(MOE_BWD2, grid, threads, lds, s>>>(a, nt));
 #undef MOE_BWD1
 #undef MOE_BWD2
-#undef MOE_BWD3
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !a.partial) return e;
   k_norm_wgrad<<<dim3((unsigned)((a.m + 31) / 32), layer ? 2 : 1), 512, 0, s>>>(a.partial, (int)grid, a.m, a.dgamma,
                                                                                layer ? a.dbeta : nullptr);
