@@ -61,6 +61,15 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
+// A 128-byte line of a row r in LDS: its chunk c of 16 bytes is stored at place
+// c ^ ((r >> 1) & 7).  Products read the same chunk of 16 successive rows in
+// one LDS cycle (256 bytes): even rows lie in the lower and odd rows in the
+// upper half of the banks, and the 8 rows of each half at 8 places, so no bank
+// is read twice (r & 7 in its place: half of the LDS cycles were conflicts).
+// The copy of lines 8 i .. 8 i + 7 makes that order by the chunk that each lane
+// fetches: lane l writes place l % 8 of line 8 i + l / 8.
+__device__ __forceinline__ int chunk_of(int i, int lane) { return (lane & 7) ^ ((4 * i + (lane >> 4)) & 7); }
+
 // global -> LDS, 16 bytes a lane from 64-bit addresses (see copy_frag).
 __device__ __forceinline__ void copy_rows(const void* p, uint32_t lds) {
   uint32_t saved;
@@ -103,8 +112,6 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   const int row0 = __builtin_amdgcn_readfirstlane(offs[e] + chunk * 16 * TB);
   const int rows = min(16 * TB, __builtin_amdgcn_readfirstlane(offs[e + 1]) - row0);
 
-  // copies: lane l brings chunk (l % 8) ^ (l / 8) of row l / 8 of the copy
-  const int c16 = 16 * ((lane & 7) ^ (lane >> 3));
   const int8_t* xsrc[CPX];
   uint32_t wsrc[CPW];
   const int8_t* const wbase = A.w + ((size_t)e * A.N + n0) * A.K;
@@ -118,12 +125,14 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   const int steps = (A.K + 127) / 128;
   const int lo = (int)((long long)steps * wave / W), hi = (int)((long long)steps * (wave + 1) / W);
   auto issue = [&](int s, int slot) {
-    const int k = min(min(s, hi - 1) * 128 + c16, A.K - 16);  // past K: any bytes of the row, multiplied by zeros
+    const int k0 = min(s, hi - 1) * 128;  // past K: any bytes of the row, multiplied by zeros
     const uint32_t at = at0 + (uint32_t)slot * STAGE;
 #pragma unroll
-    for (int j = 0; j < CPW; ++j) copy_frag(wbase, wsrc[j] + (uint32_t)k, at + (CPX + j) * 1024);
+    for (int j = 0; j < CPW; ++j) 
+      copy_frag(wbase, wsrc[j] + (uint32_t)min(k0 + 16 * chunk_of(j, lane), A.K - 16), at + (CPX + j) * 1024);
 #pragma unroll
-    for (int j = 0; j < CPX; ++j) copy_rows(xsrc[j] + k, at + j * 1024);
+    for (int j = 0; j < CPX; ++j) 
+      copy_rows(xsrc[j] + min(k0 + 16 * chunk_of(j, lane), A.K - 16), at + j * 1024);
   };
   i32x4_t acc[CB][TB] = {};
   const int rowoff = (lane & 15) * 128, quart = lane >> 4;
@@ -137,7 +146,7 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
       i32x4_t wv[2][CB], xv[2][TB];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const int at = rowoff + (((4 * ks + quart) ^ (lane & 7)) * 16);
+        const int at = rowoff + (((4 * ks + quart) ^ ((lane >> 1) & 7)) * 16);
 #pragma unroll
         for (int c = 0; c < CB; ++c) wv[ks][c] = *reinterpret_cast<const i32x4_t*>(st + (CPX + 2 * c) * 1024 + at);
 #pragma unroll
@@ -206,10 +215,7 @@ hipError_t launch_rows(const I8Args& a, bool y_bf16, hipStream_t s) {
 // A workgroup of WT x WC waves computes 32 TB WT rows by 32 CB WC channels of
 // one expert.  A stage is 128 bytes of the reduction: one cache line of every
 // row and channel of the tile, copied into LDS with 16 bytes a lane, eight
-// lines a copy, S stages in a ring.  A line's eight 16-byte chunks are stored
-// at chunk ^ (row & 7), so that the 8 lanes of one LDS cycle, which read the
-// same chunk of 8 successive rows, touch all banks once; the copy makes that
-// order by choosing each lane's source chunk.
+// lines a copy, S stages in a ring (see chunk_of for a line's order in LDS).
 template <int TB, int CB, int WT, int WC, int S>
 struct TileShape {
   static constexpr int waves = WT * WC;
@@ -238,9 +244,9 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   const int rows = min(Sh::BM, __builtin_amdgcn_readfirstlane(offs[e + 1]) - row0);
   const int n0 = nb * Sh::BN;
 
-  // copies: lane l of a copy brings chunk (l % 8) ^ (l / 8) of the copy's row
-  // l / 8 (rows past the tile's last and channels past N re-read the last one)
-  const int c16 = 16 * ((lane & 7) ^ (lane >> 3));
+  // copies: lane l of the copy of lines 8 i .. 8 i + 7 brings chunk
+  // chunk_of(i, l) of line 8 i + l / 8 (rows past the tile's last and channels
+  // past N re-read the last one)
   const int8_t* xsrc[Sh::CPX];
   uint32_t wsrc[Sh::CPW];
   const int8_t* const wbase = A.w + ((size_t)e * A.N + n0) * A.K;
@@ -263,13 +269,18 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   const int rot = rotate && A.K % 128 == 0 ? nb % steps : 0;
   auto stage_of = [&](int s) { const int r = s + rot; return r < steps ? r : r - steps; };
   auto issue = [&](int s) {
-    const int k = min(stage_of(s) * 128 + c16, A.K - 16);  // past K: any bytes of the row, multiplied by zeros
     const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);
+    const int k0 = stage_of(s) * 128;  // past K: any bytes of the row, multiplied by zeros
 #pragma unroll
-    for (int j = 0; j < Sh::CPX; ++j) copy_rows(xsrc[j] + k, at + (Sh::CPX * wave + j) * 1024);
+    for (int j = 0; j < Sh::CPX; ++j) {
+      const int i = Sh::CPX * wave + j;
+      copy_rows(xsrc[j] + min(k0 + 16 * chunk_of(i, lane), A.K - 16), at + i * 1024);
+    }
 #pragma unroll
-    for (int j = 0; j < Sh::CPW; ++j)
-      copy_frag(wbase, wsrc[j] + (uint32_t)k, at + Sh::XB + (Sh::CPW * wave + j) * 1024);
+    for (int j = 0; j < Sh::CPW; ++j) {
+      const int i = Sh::CPW * wave + j;
+      copy_frag(wbase, wsrc[j] + (uint32_t)min(k0 + 16 * chunk_of(i, lane), A.K - 16), at + Sh::XB + i * 1024);
+    }
   };
 
   i32x16_t acc[CB][TB];
@@ -283,37 +294,69 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   // operand reads: lane l takes chunk 2 ks + l / 32 of row l % 32 of a block
   const int half = lane >> 5;
   const int rowoff = (lane & 31) * 128;
-  auto step = [&](int s, int ks, bool tail) {
+  struct Frag {
+    i32x4_t x[TB], w[CB];
+  };
+  auto load = [&](Frag& f, int s, int ks) {
     const unsigned char* st = ring[s % S];
-    const int at = rowoff + (((2 * ks + half) ^ (lane & 7)) * 16);
-    i32x4_t xv[TB], wv[CB];
+    const int at = rowoff + (((2 * ks + half) ^ ((lane >> 1) & 7)) * 16);
 #pragma unroll
-    for (int c = 0; c < CB; ++c) {
-      wv[c] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + c) * 4096 + at);
-      if (tail && stage_of(s) * 128 + 32 * ks + 16 * half >= A.K) wv[c] = i32x4_t{0, 0, 0, 0};
-    }
+    for (int c = 0; c < CB; ++c) f.w[c] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + c) * 4096 + at);
 #pragma unroll
-    for (int i = 0; i < TB; ++i) xv[i] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + i) * 4096 + at);
+    for (int i = 0; i < TB; ++i) f.x[i] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + i) * 4096 + at);
+  };
+  auto multiply = [&](const Frag& f) {
 #pragma unroll
     for (int i = 0; i < TB; ++i)
 #pragma unroll
       for (int c = 0; c < CB; ++c)
-        acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[c], xv[i], acc[c][i], 0, 0, 0);
+        acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[c], f.x[i], acc[c][i], 0, 0, 0);
   };
 
+  // Every operand read is issued ahead of the products of the quarter stage
+  // before it, across the stages too: a stage's last quarter is multiplied
+  // after the barrier that frees its ring slot, while the copies into that
+  // slot and the next stage's first reads are under way.
+  Frag f0, f1;
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(min(s, last));
-  for (int s = 0; s < last; ++s) {
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
-    ring_barrier();
-    issue(min(s + S - 1, last));
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) step(s, ks, false);
-  }
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  for (int s = 0; s < S; ++s)
+    if (s <= last) issue(s);
+  if (S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 1)));
+  else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   ring_barrier();
-  const int kss = (A.K - last * 128 + 31) / 32;
-  for (int ks = 0; ks < kss; ++ks) step(last, ks, true);
+  load(f0, 0, 0);
+  for (int s = 0; s < last; ++s) {
+    load(f1, s, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(f0);
+    __builtin_amdgcn_sched_barrier(0);
+    load(f0, s, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(f1);
+    __builtin_amdgcn_sched_barrier(0);
+    load(f1, s, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(f0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    ring_barrier();
+    load(f0, s + 1, 0);
+    if (s + S <= last) issue(s + S);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(f1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  {  // the last stage: up to 128 bytes, weights past K zeroed
+    const int left = A.K - last * 128;  // (a partial stage is never rotated)
+    for (int ks = 0; 32 * ks < left; ++ks) {
+      load(f0, last, ks);
+      if (32 * ks + 16 * half >= left)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) f0.w[c] = i32x4_t{0, 0, 0, 0};
+      multiply(f0);
+    }
+  }
   __syncthreads();  // the ring is free
 
   // Epilogue: element v of acc[c][i] in lane l is channel 8 (v / 4) + 4 (l /
