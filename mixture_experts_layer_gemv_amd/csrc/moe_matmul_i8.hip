@@ -297,66 +297,70 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   struct Frag {
     i32x4_t x[TB], w[CB];
   };
-  auto load = [&](Frag& f, int s, int ks) {
-    const unsigned char* st = ring[s % S];
-    const int at = rowoff + (((2 * ks + half) ^ ((lane >> 1) & 7)) * 16);
-#pragma unroll
-    for (int c = 0; c < CB; ++c) f.w[c] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + c) * 4096 + at);
-#pragma unroll
-    for (int i = 0; i < TB; ++i) f.x[i] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + i) * 4096 + at);
-  };
-  auto multiply = [&](const Frag& f) {
-#pragma unroll
-    for (int i = 0; i < TB; ++i)
-#pragma unroll
-      for (int c = 0; c < CB; ++c)
-        acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[c], f.x[i], acc[c][i], 0, 0, 0);
-  };
-
   // Every operand read is issued ahead of the products of the quarter stage
   // before it, across the stages too: a stage's last quarter is multiplied
   // after the barrier that frees its ring slot, while the copies into that
-  // slot and the next stage's first reads are under way.
-  Frag f0, f1;
+  // slot and the next stage's first reads are under way.  LIVE: the wave's row
+  // blocks that hold rows (an expert's last tile); the others are not read or
+  // multiplied, and a wave without any only copies.
+  auto reduce = [&](auto live) {
+    constexpr int LIVE = decltype(live)::value;
+    auto load = [&](Frag& f, int s, int ks) {
+      if constexpr (LIVE > 0) {
+        const unsigned char* st = ring[s % S];
+        const int at = rowoff + (((2 * ks + half) ^ ((lane >> 1) & 7)) * 16);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) f.w[c] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + c) * 4096 + at);
+#pragma unroll
+        for (int i = 0; i < LIVE; ++i) f.x[i] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + i) * 4096 + at);
+      }
+    };
+    auto multiply = [&](const Frag& f) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < LIVE; ++i)
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+          acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[c], f.x[i], acc[c][i], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    Frag f0, f1;
+    load(f0, 0, 0);
+    for (int s = 0; s < last; ++s) {
+      load(f1, s, 1);
+      multiply(f0);
+      load(f0, s, 2);
+      multiply(f1);
+      load(f1, s, 3);
+      multiply(f0);
+      if (s + S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
+      else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+      ring_barrier();
+      load(f0, s + 1, 0);
+      if (s + S <= last) issue(s + S);
+      multiply(f1);
+    }
+    const int left = A.K - last * 128;  // the last stage: up to 128 bytes (a partial one is never rotated)
+    for (int ks = 0; 32 * ks < left; ++ks) {
+      load(f0, last, ks);
+      if (LIVE > 0 && 32 * ks + 16 * half >= left)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) f0.w[c] = i32x4_t{0, 0, 0, 0};  // weights past K
+      multiply(f0);
+    }
+  };
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (s <= last) issue(s);
   if (S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 1)));
   else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   ring_barrier();
-  load(f0, 0, 0);
-  for (int s = 0; s < last; ++s) {
-    load(f1, s, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(f0);
-    __builtin_amdgcn_sched_barrier(0);
-    load(f0, s, 2);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(f1);
-    __builtin_amdgcn_sched_barrier(0);
-    load(f1, s, 3);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(f0);
-    __builtin_amdgcn_sched_barrier(0);
-    if (s + S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
-    else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    ring_barrier();
-    load(f0, s + 1, 0);
-    if (s + S <= last) issue(s + S);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(f1);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  {  // the last stage: up to 128 bytes, weights past K zeroed
-    const int left = A.K - last * 128;  // (a partial stage is never rotated)
-    for (int ks = 0; 32 * ks < left; ++ks) {
-      load(f0, last, ks);
-      if (32 * ks + 16 * half >= left)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) f0.w[c] = i32x4_t{0, 0, 0, 0};
-      multiply(f0);
-    }
-  }
+  const int live = min(TB, (rows - wt * TB * 32 + 31) >> 5);
+  if (live == TB) reduce(std::integral_constant<int, TB>{});
+  else if (live <= 0) reduce(std::integral_constant<int, 0>{});
+  else if (TB == 4 && live == 3) reduce(std::integral_constant<int, TB == 4 ? 3 : 1>{});
+  else if (TB == 4 && live == 2) reduce(std::integral_constant<int, TB == 4 ? 2 : 1>{});
+  else reduce(std::integral_constant<int, 1>{});
   __syncthreads();  // the ring is free
 
   // Epilogue: element v of acc[c][i] in lane l is channel 8 (v / 4) + 4 (l /
