@@ -86,10 +86,10 @@ def test_dense(R, K, N, out):
 
 
 # wide enough for every tile shape the launch chooses from on 256 CUs: 256 x
-# 256, 128 x 256, 64 x 128, 64 x 64 and 32 x 256 rows by channels, and the two
+# 256, 128 x 256, 128 x 128, 64 x 128, 64 x 64 and 32 x 256 rows by channels, and the two
 # kernels for few rows; K with and without a partial last stage
 WIDE = [(4100, 144, 4104), (3841, 384, 4360), (2049, 272, 4104), (2300, 256, 3080), (515, 208, 4008), (450, 640, 4104),
-        (60, 176, 12296), (64, 256, 12808), (31, 400, 2056), (32, 2064, 136), (16, 4112, 1032), (40, 2064, 72)]
+        (300, 400, 8200), (1030, 272, 3080), (60, 176, 12296), (64, 256, 12808), (31, 400, 2056), (32, 2064, 136), (16, 4112, 1032), (40, 2064, 72)]
 
 
 @pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
