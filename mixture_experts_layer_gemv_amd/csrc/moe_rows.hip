@@ -187,7 +187,7 @@ __device__ __forceinline__ float team_sum(float v, int NT, int first, float* slo
 // sqrt(mean((x - mu)^2) + eps).  gamma and beta stay in registers from row to
 // row; the next row is loaded while this one is summed.
 template <bool BF16, int V, bool LAYER>
-__global__ __launch_bounds__(V == 1 ? 256 : 1024) void k_norm_fwd(const NormArgs A, int NT) {
+__global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
   __shared__ float red[2][16];
   const int team = threadIdx.x / NT, teams = blockDim.x / NT, tid = threadIdx.x - team * NT;
   const int first = team * NT >> 6;  // the team's first wave
@@ -574,8 +574,7 @@ int norm_threads(int m, int V) {
   const int n = (m + 8 * V - 1) / (8 * V);
   return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : (n + 63) / 64 * 64;
 }
-int norm_fwd_vecs(int m) { return m <= 2048 ? 1 : 2; }
-int norm_bwd_vecs(int m) { return m <= 8192 ? 1 : 2; }
+int norm_vecs(int m) { return m <= 8192 ? 1 : 2; }
 // Teams of a block.
 int norm_fwd_teams(int nt) { return nt <= 256 ? 256 / nt : 1; }
 int norm_bwd_teams(int nt) { return nt <= 512 ? 512 / nt : 1; }
@@ -593,8 +592,8 @@ int norm_bwd_teams(int nt) { return nt <= 512 ? 512 / nt : 1; }
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
-  const int V = norm_fwd_vecs(a.m), nt = norm_threads(a.m, V), teams = norm_fwd_teams(nt), threads = nt * teams;
-  const long long blocks = ((long long)a.T + teams - 1) / teams, most = (long long)cus * (2048 / threads);
+  const int V = norm_vecs(a.m), nt = norm_threads(a.m, V), teams = norm_fwd_teams(nt), threads = nt * teams;
+  const long long blocks = ((long long)a.T + teams - 1) / teams, most = (long long)cus * (V == 1 ? 2048 / threads : 1);
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
 #define MOE_FWD1(B, L) k_norm_fwd<B, 1, L>
 #define MOE_FWD2(B, L) k_norm_fwd<B, 2, L>
@@ -606,8 +605,8 @@ hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus
 }
 
 int norm_backward_blocks(int T, int m, int cus) {
-  const int nt = norm_threads(m, norm_bwd_vecs(m)), teams = norm_bwd_teams(nt);
-  const long long steps = ((long long)T + teams - 1) / teams, most = (long long)cus * (nt <= 512 ? 2 : 1);
+  const int nt = norm_threads(m, norm_vecs(m)), teams = norm_bwd_teams(nt);
+  const long long steps = ((long long)T + teams - 1) / teams, most = (long long)cus * (nt < 256 ? 2 : 1);
   if (steps <= most) return (int)steps;
   const long long per = (steps + most - 1) / most;  // the same number of steps for every block but the last
   return (int)((steps + per - 1) / per);
@@ -616,7 +615,7 @@ int norm_backward_blocks(int T, int m, int cus) {
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
-  const int V = norm_bwd_vecs(a.m), nt = norm_threads(a.m, V), threads = nt * norm_bwd_teams(nt);
+  const int V = norm_vecs(a.m), nt = norm_threads(a.m, V), threads = nt * norm_bwd_teams(nt);
   const unsigned grid = (unsigned)norm_backward_blocks(a.T, a.m, cus);
   const size_t lds = threads > (nt < 64 ? 64 : nt) ? 2 * sizeof(float) * (size_t)a.m : 0;  // at most 2048 columns
 #define MOE_BWD1(B, L) k_norm_bwd<B, 1, L>
