@@ -268,19 +268,21 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   // come last.
   const int rot = rotate && A.K % 128 == 0 ? nb % steps : 0;
   auto stage_of = [&](int s) { const int r = s + rot; return r < steps ? r : r - steps; };
-  auto issue = [&](int s) {
+  // copy j of the wave's CP of stage s
+  auto issue_one = [&](int s, int j) {
     const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);
     const int k0 = stage_of(s) * 128;  // past K: any bytes of the row, multiplied by zeros
-#pragma unroll
-    for (int j = 0; j < Sh::CPX; ++j) {
+    if (j < Sh::CPX) {
       const int i = Sh::CPX * wave + j;
       copy_rows(xsrc[j] + min(k0 + 16 * chunk_of(i, lane), A.K - 16), at + i * 1024);
+    } else {
+      const int i = Sh::CPW * wave + j - Sh::CPX;
+      copy_frag(wbase, wsrc[j - Sh::CPX] + (uint32_t)min(k0 + 16 * chunk_of(i, lane), A.K - 16), at + Sh::XB + i * 1024);
     }
+  };
+  auto issue = [&](int s) {
 #pragma unroll
-    for (int j = 0; j < Sh::CPW; ++j) {
-      const int i = Sh::CPW * wave + j;
-      copy_frag(wbase, wsrc[j] + (uint32_t)min(k0 + 16 * chunk_of(i, lane), A.K - 16), at + Sh::XB + i * 1024);
-    }
+    for (int j = 0; j < Sh::CP; ++j) issue_one(s, j);
   };
 
   i32x16_t acc[CB][TB];
@@ -326,18 +328,40 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
     };
     Frag f0, f1;
     load(f0, 0, 0);
-    for (int s = 0; s < last; ++s) {
+    int s = 0;
+    for (; s + S <= last; ++s) {
       load(f1, s, 1);
       multiply(f0);
       load(f0, s, 2);
       multiply(f1);
       load(f1, s, 3);
       multiply(f0);
-      if (s + S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
-      else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
       ring_barrier();
       load(f0, s + 1, 0);
-      if (s + S <= last) issue(s + S);
+      __builtin_amdgcn_sched_barrier(0);
+      // a copy after each product: together they would leave the matrix cores
+      // idle for as long as they take to issue
+#pragma unroll
+      for (int j = 0; j < (LIVE * CB > Sh::CP ? LIVE * CB : Sh::CP); ++j) {
+        if (j < LIVE * CB) {
+          const int i = j / CB, c = j % CB;
+          acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f1.w[c], f1.x[i], acc[c][i], 0, 0, 0);
+        }
+        if (j < Sh::CP) issue_one(s + S, j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    for (; s < last; ++s) {
+      load(f1, s, 1);
+      multiply(f0);
+      load(f0, s, 2);
+      multiply(f1);
+      load(f1, s, 3);
+      multiply(f0);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+      ring_barrier();
+      load(f0, s + 1, 0);
       multiply(f1);
     }
     const int left = A.K - last * 128;  // the last stage: up to 128 bytes (a partial one is never rotated)
