@@ -307,70 +307,63 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   // multiplied, and a wave without any only copies.
   auto reduce = [&](auto live) {
     constexpr int LIVE = decltype(live)::value;
-    auto load = [&](Frag& f, int s, int ks) {
-      if constexpr (LIVE > 0) {
-        const unsigned char* st = ring[s % S];
-        const int at = rowoff + (((2 * ks + half) ^ ((lane >> 1) & 7)) * 16);
-#pragma unroll
-        for (int c = 0; c < CB; ++c) f.w[c] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + c) * 4096 + at);
-#pragma unroll
-        for (int i = 0; i < LIVE; ++i) f.x[i] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + i) * 4096 + at);
-      }
+    // operand j of quarter ks of stage s: the channel blocks, then the row blocks
+    auto load_one = [&](Frag& f, int s, int ks, int j) {
+      const unsigned char* st = ring[s % S];
+      const int at = rowoff + (((2 * ks + half) ^ ((lane >> 1) & 7)) * 16);
+      if (j < CB) f.w[j] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + j) * 4096 + at);
+      else f.x[j - CB] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + j - CB) * 4096 + at);
     };
-    auto multiply = [&](const Frag& f) {
-      __builtin_amdgcn_sched_barrier(0);
+    constexpr int READS = LIVE ? CB + LIVE : 0, PRODUCTS = LIVE * CB;
+    // The products of `f`, and after each one a read of the next quarter's
+    // operands (`next`, quarter ks of stage s) and, with COPY, a copy of stage
+    // `cs`: reads and copies issued together would leave the matrix cores idle
+    // for as long as they take to issue.
+    auto pass = [&](const Frag& f, Frag& next, int s, int ks, auto copy, int cs) {
+      constexpr int COPIES = decltype(copy)::value ? Sh::CP : 0;
+      constexpr int N = PRODUCTS > READS ? (PRODUCTS > COPIES ? PRODUCTS : COPIES) : (READS > COPIES ? READS : COPIES);
 #pragma unroll
-      for (int i = 0; i < LIVE; ++i)
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-          acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[c], f.x[i], acc[c][i], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    Frag f0, f1;
-    load(f0, 0, 0);
-    int s = 0;
-    for (; s + S <= last; ++s) {
-      load(f1, s, 1);
-      multiply(f0);
-      load(f0, s, 2);
-      multiply(f1);
-      load(f1, s, 3);
-      multiply(f0);
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
-      ring_barrier();
-      load(f0, s + 1, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      // a copy after each product: together they would leave the matrix cores
-      // idle for as long as they take to issue
-#pragma unroll
-      for (int j = 0; j < (LIVE * CB > Sh::CP ? LIVE * CB : Sh::CP); ++j) {
-        if (j < LIVE * CB) {
-          const int i = j / CB, c = j % CB;
-          acc[c][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f1.w[c], f1.x[i], acc[c][i], 0, 0, 0);
-        }
-        if (j < Sh::CP) issue_one(s + S, j);
+      for (int j = 0; j < N; ++j) {
+        if (j < READS) load_one(next, s, ks, j);
+        if (j < PRODUCTS)
+          acc[j % CB][j / CB] =
+              __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[j % CB], f.x[j / CB], acc[j % CB][j / CB], 0, 0, 0);
+        if (j < COPIES) issue_one(cs, j);
         __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    const std::false_type none{};
+    Frag f0, f1;
+#pragma unroll
+    for (int j = 0; j < READS; ++j) load_one(f0, 0, 0, j);
+    int s = 0;
+    for (; s + S <= last; ++s) {
+      pass(f0, f1, s, 1, none, 0);
+      pass(f1, f0, s, 2, none, 0);
+      pass(f0, f1, s, 3, none, 0);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
+      ring_barrier();
+      pass(f1, f0, s + 1, 0, std::true_type{}, s + S);
     }
     for (; s < last; ++s) {
-      load(f1, s, 1);
-      multiply(f0);
-      load(f0, s, 2);
-      multiply(f1);
-      load(f1, s, 3);
-      multiply(f0);
+      pass(f0, f1, s, 1, none, 0);
+      pass(f1, f0, s, 2, none, 0);
+      pass(f0, f1, s, 3, none, 0);
       __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
       ring_barrier();
-      load(f0, s + 1, 0);
-      multiply(f1);
+      pass(f1, f0, s + 1, 0, none, 0);
     }
     const int left = A.K - last * 128;  // the last stage: up to 128 bytes (a partial one is never rotated)
     for (int ks = 0; 32 * ks < left; ++ks) {
-      load(f0, last, ks);
+#pragma unroll
+      for (int j = 0; j < READS; ++j) load_one(f0, last, ks, j);
       if (LIVE > 0 && 32 * ks + 16 * half >= left)
 #pragma unroll
         for (int c = 0; c < CB; ++c) f0.w[c] = i32x4_t{0, 0, 0, 0};  // weights past K
-      multiply(f0);
+#pragma unroll
+      for (int j = 0; j < PRODUCTS; ++j)
+        acc[j % CB][j / CB] =
+            __builtin_amdgcn_mfma_i32_32x32x32_i8(f0.w[j % CB], f0.x[j / CB], acc[j % CB][j / CB], 0, 0, 0);
     }
   };
 #pragma unroll
