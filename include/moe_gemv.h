@@ -495,7 +495,7 @@ moe_status moe_combine_rows_backward(const void* dy, int dy_dtype, const void* y
  *   scale[t] = 2^X, X the smallest integer with max_i |x[t][i]| <= 127 * 2^X;
  *   codes[t][i] = round-half-even(x[t][i] / scale[t])
  *  x  device bf16 [T][m] (finite values), m a multiple of 64, 16-byte aligned;
- *  codes  device int8 [T][m], 16-byte aligned;  scale  device fp32 [T].
+ *  codes  device int8 [T][m], 16-byte aligned;  scale  device fp32 [T];  T < 2^24.
  * Errors: INVALID_ARG, UNSUPPORTED, HIP.
  */
 moe_status moe_quantize_codes_i8(const void* x, int T, int m, int8_t* codes, float* scale, void* stream);
@@ -513,12 +513,13 @@ moe_status moe_quantize_codes_i8(const void* x, int T, int m, int8_t* codes, flo
  *             (w1 and w2 of moe_weights_create are [E][K][N]).
  *  w_scale    device fp32 [E][N].
  *  offsets    device int32 [E+1] from moe_dispatch, or NULL: E must be 1 and all rows
- *             are its.  Values are read as if clamped to [0, rows]; rows of no range
- *             are left as they were.
+ *             are its.  Values are read as if clamped to [0, rows], a decreasing one
+ *             as its predecessor; rows of no range are left as they were.
  *  perm       device int32 [rows] from moe_dispatch, or NULL (T must equal rows).
  *             perm[r] / topk is read as if clamped to [0, T).
  *  y          device [rows][N] in y_dtype (MOE_F32 or MOE_BF16).
- *  K <= 131056; 1 <= E <= 64; x, w, w_scale and y 16-byte aligned.
+ *  K <= 131056; 1 <= E <= 64; (rows / 64 + E) * ceil(N / 16) < 2^24; x, w, w_scale
+ *  and y 16-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, HIP.
  */
 moe_status moe_matmul_i8(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,

@@ -1815,6 +1815,7 @@ moe_status moe_combine_rows_backward(const void* dy, int dy_dtype, const void* y
 moe_status moe_quantize_codes_i8(const void* x, int T, int m, int8_t* codes, float* scale, void* stream) {
   if (T < 0 || m <= 0) return fail(MOE_ERR_INVALID_ARG, "bad sizes T=%d m=%d", T, m);
   if (m % 64) return fail(MOE_ERR_UNSUPPORTED, "m=%d must be a multiple of 64", m);
+  if (T >= 1 << 24) return fail(MOE_ERR_UNSUPPORTED, "T=%d needs 2^32 threads or more", T);
   if (T == 0) return ok();
   if (!x || !codes || !scale) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
   if (!aligned16(x) || !aligned16(codes)) return fail(MOE_ERR_INVALID_ARG, "x/codes must be 16-byte aligned");

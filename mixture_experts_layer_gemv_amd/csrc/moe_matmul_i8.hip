@@ -83,7 +83,6 @@ __device__ __forceinline__ void copy_rows(const void* p, uint32_t lds) {
       : "memory");
 }
 
-
 // Upper bound on the row blocks of BM rows.
 long long row_blocks(const I8Args& a, int BM) {
   return a.offsets ? (long long)a.R / BM + (a.R < a.E ? a.R : a.E) : ((long long)a.R + BM - 1) / BM;
@@ -94,7 +93,10 @@ long long row_blocks(const I8Args& a, int BM) {
 // A workgroup owns 16 CB output channels and up to 16 TB rows of one expert;
 // its W waves split the reduction and add their int32 sums in LDS.  Each wave
 // copies its own lines through a private ring of S stages (128 bytes of every
-// row and channel), so no wave waits for another before the final sum.
+// row and channel), so no wave waits for another before the final sum.  The
+// weights' bytes bound it: 16 x 4096 x 14336 takes 11.1 us, 5.3 TB/s (a large
+// copy reaches 5.0 on this card).  Weights loaded straight into registers,
+// half a line an instruction, took 13.5 us.
 template <int TB, int CB, int W, int S, bool YB>
 __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   constexpr int CPX = 2 * TB, CPW = 2 * CB, CP = CPX + CPW;
@@ -128,10 +130,10 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
     const int k0 = min(s, hi - 1) * 128;  // past K: any bytes of the row, multiplied by zeros
     const uint32_t at = at0 + (uint32_t)slot * STAGE;
 #pragma unroll
-    for (int j = 0; j < CPW; ++j) 
+    for (int j = 0; j < CPW; ++j)
       copy_frag(wbase, wsrc[j] + (uint32_t)min(k0 + 16 * chunk_of(j, lane), A.K - 16), at + (CPX + j) * 1024);
 #pragma unroll
-    for (int j = 0; j < CPX; ++j) 
+    for (int j = 0; j < CPX; ++j)
       copy_rows(xsrc[j] + min(k0 + 16 * chunk_of(j, lane), A.K - 16), at + j * 1024);
   };
   i32x4_t acc[CB][TB] = {};
@@ -216,6 +218,14 @@ hipError_t launch_rows(const I8Args& a, bool y_bf16, hipStream_t s) {
 // one expert.  A stage is 128 bytes of the reduction: one cache line of every
 // row and channel of the tile, copied into LDS with 16 bytes a lane, eight
 // lines a copy, S stages in a ring (see chunk_of for a line's order in LDS).
+//
+// What bounds it: large products (256 x 256 tiles, two waves per SIMD, 128 x
+// 64 each) the power of products, LDS reads and copies together.  8192 x 4096
+// x 14336 takes 408 us, 2.36 POP/s; the products alone 283 us, products and
+// LDS reads 350 us, the copies alone 290 us, while the clock falls to 1.8 GHz.
+// A deeper ring (96 KiB under way instead of 64) and four waves of 128 x 128
+// (a third fewer LDS reads) measured 2 and 3 % slower.  Products of few rows
+// (32 x 256 tiles) stream their weights at 5.6 TB/s.
 template <int TB, int CB, int WT, int WC, int S>
 struct TileShape {
   static constexpr int waves = WT * WC;
@@ -227,7 +237,8 @@ struct TileShape {
 };
 
 template <int TB, int CB, int WT, int WC, int S, bool YB>
-__global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg, int rotate) {
+__global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg,
+                                                                                                     int rotate) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   __shared__ __attribute__((aligned(1024))) unsigned char ring[S][Sh::XB + Sh::WB];
   __shared__ int offs[kMaxExperts + 1];
@@ -264,7 +275,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   // Where a weight tile is read once (rotate), neighbouring column blocks walk
   // the reduction from different stages: in step with one another they read
   // the same offset of rows a power of two apart, few of the memory's channels
-  // (474 MB of decode weights: 94 against 86 us).  A partial last stage has to
+  // (474 MB of decode weights: 100 against 84 us).  A partial last stage has to
   // come last.
   const int rot = rotate && A.K % 128 == 0 ? nb % steps : 0;
   auto stage_of = [&](int s) { const int r = s + rot; return r < steps ? r : r - steps; };
@@ -418,8 +429,11 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
         else
           *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
       }
-    constexpr int LPR = RB / 16;     // lanes per row
-    constexpr int RPI = 64 / LPR;    // rows per store
+    constexpr int LPR = RB / 16;   // lanes per row
+    constexpr int RPI = 64 / LPR;  // rows per store
+    // other lanes of the wave wrote what a lane reads (a wave's LDS accesses
+    // take place in order; the compiler must keep them so across the types)
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int q = 0; q < 32 / RPI; ++q) {
       const int rr = q * RPI + lane / LPR, col = lane % LPR;
@@ -428,6 +442,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
       if (rb + rr < rows && n < A.N)
         *reinterpret_cast<uint4*>(static_cast<char*>(A.y) + ((size_t)(row0 + rb + rr) * A.N + n) * ES) = v;
     }
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -453,22 +468,22 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
   // product, but one round of too few tiles leaves CUs idle.
   const long long experts = a.R < a.E ? a.R : a.E, avg = (a.R + experts - 1) / experts, enough = 3 * cus / 4;
   auto items = [&](int BM, int BN) { return experts * ((avg + BM - 1) / BM) * ((a.N + BN - 1) / BN); };
-  const int cg = 4;  // column blocks that share their rows in an XCD's L2 (1, 2 and 8: within 2 %)
-  // 16384 rows of 8 experts, 4096 x 14336: 256 x 256 0.97, 128 x 256 1.12 ms; 128 rows each: 121 and 126 us
+  const int cg = 4;  // column blocks that share their rows in an XCD's L2 (2 and 8: within 2 %; 1: 10 % slower)
+  // 16384 rows of 8 experts, 4096 x 14336: 0.92, 128 x 256 1.05 ms; 128 rows each: 119 and 126 us
   if (avg > 112 && items(256, 256) >= enough) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, avg <= 192, s);
-  // 64 rows each of 8 experts: 92 us, 64 x 128 106 us; 2048 x 4096 x 4096: 39.5 us, 256 x 256 51 us
+  // 64 rows each of 8 experts: 93, 64 x 128 106 us; 2048 x 4096 x 4096 (128 items of 256 x 256): 37 and 43 us
   if (avg > 48 && items(128, 256) >= enough) return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, avg <= 128, s);
-  // 1003 x 6400 x 4096: 35 us, 128 x 256 48 us, 64 x 128 38 us
+  // 1003 x 6400 x 4096: 33 us, 128 x 256 40 us, 64 x 128 38 us
   if (avg > 64 && items(128, 128) >= enough) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, s);
-  // 512 x 4096 x 4096: 16 us, 128 x 128 19 us
+  // 512 x 4096 x 4096: 16.1 us, 128 x 128 17.3 us
   if (avg > 32 && items(64, 128) >= enough) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, s);
-  // 16 rows each of 8 experts, 4096 x 14336: 84 us, 64 x 64 92 us; 16 x 4096 x 14336 (56 items): 25 and 11.6 us
+  // 16 rows each of 8 experts, 4096 x 14336: 82 us, 64 x 64 88 us; 16 x 4096 x 14336 (56 items): 24 and 11 us
   if (avg <= 32 && 4 * items(32, 256) >= 5 * cus) return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, 1, s);
-  // 64 x 4096 x 14336: 12.1 us, 32 rows on private rings 20 us
+  // 64 x 4096 x 14336: 12 us, 32 rows on private rings 22 us
   if ((avg > 16 || a.E > 1) && items(64, 64) >= enough) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, 0, s);
-  // 16 x 14336 x 4096 (64 items of 64 channels): 11.5 us, 64 x 64 30 us
+  // 16 x 14336 x 4096 (64 items of 64 channels): 11.4 us, 64 x 64 29 us
   if (avg <= 16) return launch_rows<1, 2, 4, 2>(a, y_bf16, s);
-  // 64 x 14336 x 4096: 14 us, 64 x 64 31 us
+  // 64 x 14336 x 4096: 13.7 us, 64 x 64 29.5 us
   return launch_rows<2, 2, 8, 1>(a, y_bf16, s);
 }
 

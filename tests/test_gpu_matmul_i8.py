@@ -175,10 +175,38 @@ def test_rows_of_no_range_and_clamped_inputs(R):
     wild = torch.tensor([-5, 3, 2**31 - 1, R + 7], dtype=torch.int32, device="cuda")  # [0,3) [3,R) [R,R)
     tame = torch.tensor([0, 3, R, R], dtype=torch.int32, device="cuda")
     check(run(x, sx, w, sw, wild, None, 1, R, F32), exact(x, sx, w, sw, tame, None, 1, R), F32)
+    falling = torch.tensor([2, 5, 3, R], dtype=torch.int32, device="cuda")  # [2,5) [5,5) [5,R)
+    tame = torch.tensor([2, 5, 5, R], dtype=torch.int32, device="cuda")
+    check(run(x, sx, w, sw, falling, None, 1, R, F32), exact(x, sx, w, sw, tame, None, 1, R), F32)
+    tame = torch.tensor([0, 3, R, R], dtype=torch.int32, device="cuda")
     perm = torch.arange(R, dtype=torch.int32, device="cuda")
     perm[0], perm[1], perm[R - 1] = -7, R + 100, 2**31 - 1
     tame_p = perm.clamp(0, R - 1)
     check(run(x, sx, w, sw, tame, perm, 1, R, F32), exact(x, sx, w, sw, tame, tame_p, 1, R), F32)
+
+
+@pytest.mark.parametrize("R", [9, 300])
+def test_gathered_rows_of_one_matrix(R):
+    """A permutation without offsets: E = 1."""
+    K, N, T = 208, 264, 7
+    x, w, sx, sw = codes((T, K), 1), codes((1, N, K), 2), scales((T,), 3), scales((1, N), 4)
+    perm = torch.randint(0, 3 * T, (R,), dtype=torch.int32, device="cuda", generator=torch.Generator("cuda").manual_seed(R))
+    check(run(x, sx, w, sw, None, perm, 3, R, BF16), exact(x, sx, w, sw, None, perm, 3, R), BF16)
+
+
+@pytest.mark.parametrize("E", [64, 63])
+def test_many_experts_with_wild_offsets(E):
+    """Every entry of the offsets counts, the last of 65 included, and none is trusted."""
+    K, N, R = 64, 40, 500
+    x, w, sx, sw = codes((R, K), 1), codes((E, N, K), 2), scales((R,), 3), scales((E, N), 4)
+    g = np.random.default_rng(E)
+    off = g.integers(-100, R + 100, E + 1).astype(np.int32)
+    tame = np.maximum.accumulate(np.clip(off, 0, R))
+    check(run(x, sx, w, sw, torch.from_numpy(off).cuda(), None, 1, R, F32),
+          exact(x, sx, w, sw, torch.from_numpy(tame), None, 1, R), F32)
+    off = np.sort(g.integers(0, R + 1, E + 1)).astype(np.int32)
+    check(run(x, sx, w, sw, torch.from_numpy(off).cuda(), None, 1, R, F32),
+          exact(x, sx, w, sw, torch.from_numpy(off), None, 1, R), F32)
 
 
 def test_same_token_twice():

@@ -113,6 +113,7 @@ def test_assignment_operators(M, fn):
 def test_quantize_codes(M):
     L = M.lib()
     assert L.moe_quantize_codes_i8(FAKE, 4, 96, FAKE, FAKE, Z) == M.MOE_ERR_UNSUPPORTED
+    assert L.moe_quantize_codes_i8(FAKE, 1 << 24, 64, FAKE, FAKE, Z) == M.MOE_ERR_UNSUPPORTED
     for a in [(Z, 4, 64, FAKE, FAKE), (FAKE, 4, 64, Z, FAKE), (FAKE, 4, 64, FAKE, Z), (FAKE + 8, 4, 64, FAKE, FAKE),
               (FAKE, 4, 64, FAKE + 8, FAKE), (FAKE, -1, 64, FAKE, FAKE), (FAKE, 4, 0, FAKE, FAKE)]:
         assert L.moe_quantize_codes_i8(*a, Z) == M.MOE_ERR_INVALID_ARG, a
