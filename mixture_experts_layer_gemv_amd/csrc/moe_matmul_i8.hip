@@ -24,30 +24,65 @@ typedef int i32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-// The experts' row offsets into LDS: clamped to [0, R], a decreasing entry
-// counting as its predecessor, so that the ranges are disjoint and in bounds
-// whatever the caller's array holds.
-__device__ __forceinline__ void load_offsets(const I8Args& A, int* offs) {
-  if (threadIdx.x == 0 && !A.offsets) {
-    offs[0] = 0;
-    offs[1] = A.R;
-  }
-  if (A.offsets && threadIdx.x < 64) {  // one wave: entries lane and, for the last lane, 64
-    const int lane = threadIdx.x;
-    int o = lane <= A.E ? A.offsets[lane] : 0;
-    o = o < 0 ? 0 : (o > A.R ? A.R : o);
+// One (expert, row block, column block) of a launch.
+struct Item {
+  int e, mb, nb;   // e < 0: none
+  int row0, rows;  // the block's first row and its rows
+};
+
+// Item L of the launch's work order (see gemm_item; cg = 0: row blocks
+// outermost), found by every wave for itself: each lane holds an expert.  The
+// offsets are clamped to [0, R], a decreasing entry counting as its
+// predecessor, so that the ranges are disjoint and in bounds whatever the
+// caller's array holds.  spread: L is the block's number, dealt evenly over
+// the XCDs (xcd_item); else it is the item.
+__device__ __forceinline__ Item find_item(const I8Args& A, int BM, int NBL, int cg, int L, bool spread) {
+  Item it{-1, 0, 0, 0, 0};
+  int e = 0, lo = 0, hi = A.R, before = 0;  // the item's expert, its rows, the items before it
+  if (!A.offsets) {
+    const int total = (hi + BM - 1) / BM * NBL;
+    if (spread) L = xcd_item(L, total, 0);
+    if (L < 0 || L >= total) return it;
+  } else {
+    const int lane = threadIdx.x & 63;
+    auto clamped = [&](int i) { return min(max(i <= A.E ? A.offsets[i] : 0, 0), A.R); };
+    int first = clamped(lane);
+    const int next = clamped(lane + 1);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int p = __shfl_up(o, d, 64);
-      if (lane >= d && p > o) o = p;
+      const int p = __shfl_up(first, d, 64);
+      if (lane >= d) first = max(first, p);
     }
-    if (lane <= A.E) offs[lane] = o;
-    if (lane == 63 && A.E == 64) {
-      const int last = A.offsets[64];
-      offs[64] = last < o ? o : (last > A.R ? A.R : last);
+    const int end = max(first, next);
+    const int items = lane < A.E ? (end - first + BM - 1) / BM * NBL : 0;
+    int sum = items;  // of the experts up to this one
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int p = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += p;
     }
+    const int total = __builtin_amdgcn_readlane(sum, 63);
+    if (spread) L = xcd_item(L, total, 0);
+    if (L < 0 || L >= total) return it;
+    e = __builtin_ctzll(__ballot(L < sum));
+    before = __builtin_amdgcn_readlane(sum - items, e);
+    lo = __builtin_amdgcn_readlane(first, e);
+    hi = __builtin_amdgcn_readlane(end, e);
   }
-  __syncthreads();
+  const int blocks = (hi - lo + BM - 1) / BM, li = L - before;
+  if (cg) {
+    const int g = li / (blocks * cg), rem = li - g * blocks * cg;
+    const int gw = min(NBL - g * cg, cg);
+    it.mb = rem / gw;
+    it.nb = g * cg + (rem - it.mb * gw);
+  } else {
+    it.mb = li / NBL;
+    it.nb = li - it.mb * NBL;
+  }
+  it.e = e;
+  it.row0 = lo + it.mb * BM;
+  it.rows = min(BM, hi - it.row0);
+  return it;
 }
 
 // The x row of output row r, kept inside [0, T).
@@ -104,15 +139,11 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   constexpr int STAGE = CP * 1024;
   constexpr int RING = W * S * STAGE, PART = W * CB * TB * 1024;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[RING > PART ? RING : PART];
-  __shared__ int offs[kMaxExperts + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  load_offsets(A, offs);
-  int e, chunk, npairs;
-  if (!skinny_pair(offs, A.E, 16 * TB, (int)(blockIdx.x / (unsigned)cols), &e, &chunk, &npairs)) return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  const int n0 = (int)(blockIdx.x % (unsigned)cols) * 16 * CB;
-  const int row0 = __builtin_amdgcn_readfirstlane(offs[e] + chunk * 16 * TB);
-  const int rows = min(16 * TB, __builtin_amdgcn_readfirstlane(offs[e + 1]) - row0);
+  // row blocks outermost: neighbouring workgroups, on different XCDs, read neighbouring channels
+  const Item it = find_item(A, 16 * TB, cols, 0, (int)blockIdx.x, false);
+  if (it.e < 0) return;
+  const int e = it.e, n0 = it.nb * 16 * CB, row0 = it.row0, rows = it.rows;
 
   const int8_t* xsrc[CPX];
   uint32_t wsrc[CPW];
@@ -241,19 +272,12 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
                                                                                                      int rotate) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   __shared__ __attribute__((aligned(1024))) unsigned char ring[S][Sh::XB + Sh::WB];
-  __shared__ int offs[kMaxExperts + 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WC, wc = wave % WC;
-  load_offsets(A, offs);
-  const int NBL = (A.N + Sh::BN - 1) / Sh::BN;
-  int e, mb, nb;
-  const int L = xcd_item(blockIdx.x, gemm_items(offs, A.E, Sh::BM, NBL), 0);
-  if (L < 0 || !gemm_item(offs, A.E, Sh::BM, NBL, cg, L, &e, &mb, &nb)) return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  const int row0 = __builtin_amdgcn_readfirstlane(offs[e]) + mb * Sh::BM;
-  const int rows = min(Sh::BM, __builtin_amdgcn_readfirstlane(offs[e + 1]) - row0);
-  const int n0 = nb * Sh::BN;
+  const Item it = find_item(A, Sh::BM, (A.N + Sh::BN - 1) / Sh::BN, cg, (int)blockIdx.x, true);
+  if (it.e < 0) return;
+  const int e = it.e, row0 = it.row0, rows = it.rows, n0 = it.nb * Sh::BN;
 
   // copies: lane l of the copy of lines 8 i .. 8 i + 7 brings chunk
   // chunk_of(i, l) of line 8 i + l / 8 (rows past the tile's last and channels
@@ -275,10 +299,9 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   // Where a weight tile is read once (rotate), neighbouring column blocks walk
   // the reduction from different stages: in step with one another they read
   // the same offset of rows a power of two apart, few of the memory's channels
-  // (474 MB of decode weights: 100 against 84 us).  A partial last stage has to
-  // come last.
-  const int rot = rotate && A.K % 128 == 0 ? nb % steps : 0;
-  auto stage_of = [&](int s) { const int r = s + rot; return r < steps ? r : r - steps; };
+  // (474 MB of decode weights: 100 against 84 us).  A partial stage stays the last.
+  const int full = A.K / 128, rot = rotate && full ? it.nb % full : 0;
+  auto stage_of = [&](int s) { return s >= full ? s : (s + rot < full ? s + rot : s + rot - full); };
   // copy j of the wave's CP of stage s
   auto issue_one = [&](int s, int j) {
     const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);
@@ -364,7 +387,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
       ring_barrier();
       pass(f1, f0, s + 1, 0, none, 0);
     }
-    const int left = A.K - last * 128;  // the last stage: up to 128 bytes (a partial one is never rotated)
+    const int left = A.K - last * 128;  // the last stage: up to 128 bytes
     for (int ks = 0; 32 * ks < left; ++ks) {
 #pragma unroll
       for (int j = 0; j < READS; ++j) load_one(f0, last, ks, j);
