@@ -488,22 +488,30 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
     return hipErrorInvalidValue;
   // The largest tile that still gives three quarters of the CUs an item, for
   // experts of the mean row count: a tile reads (1 / BM + 1 / BN) bytes per
-  // product, but one round of too few tiles leaves CUs idle.
-  const long long experts = a.R < a.E ? a.R : a.E, avg = (a.R + experts - 1) / experts, enough = 3 * cus / 4;
+  // product, but one round of too few tiles leaves CUs idle.  Half of the CUs
+  // are enough where the next smaller tile would need a second round.
+  const long long experts = a.R < a.E ? a.R : a.E, avg = (a.R + experts - 1) / experts;
   auto items = [&](int BM, int BN) { return experts * ((avg + BM - 1) / BM) * ((a.N + BN - 1) / BN); };
+  auto enough = [&](long long n, long long finer) { return 4 * n >= 3 * cus || (2 * n >= cus && finer > cus); };
+  const long long n256 = items(256, 256), n128 = items(128, 256), n128s = items(128, 128);
   const int cg = 4;  // column blocks that share their rows in an XCD's L2 (2 and 8: within 2 %; 1: 10 % slower)
-  // 16384 rows of 8 experts, 4096 x 14336: 0.92, 128 x 256 1.05 ms; 128 rows each: 119 and 126 us
-  if (avg > 112 && items(256, 256) >= enough) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, avg <= 192, s);
+  // 16384 rows of 8 experts, 4096 x 14336: 0.91, 128 x 256 1.05 ms; 128 rows each: 120 and 126 us;
+  // 5565 x 2832 x 1680 (154 items, 308 of 128 x 256): 39 and 53 us
+  if (avg > 112 && enough(n256, n128)) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, avg <= 192, s);
   // 64 rows each of 8 experts: 93, 64 x 128 106 us; 2048 x 4096 x 4096 (128 items of 256 x 256): 37 and 43 us
-  if (avg > 48 && items(128, 256) >= enough) return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, avg <= 128, s);
+  if (avg > 48 && enough(n128, n128s)) return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, avg <= 128, s);
   // 1003 x 6400 x 4096: 33 us, 128 x 256 40 us, 64 x 128 38 us
-  if (avg > 64 && items(128, 128) >= enough) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, s);
+  if (avg > 64 && 4 * n128s >= 3 * cus) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, s);
   // 512 x 4096 x 4096: 16.1 us, 128 x 128 17.3 us
-  if (avg > 32 && items(64, 128) >= enough) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, s);
-  // 16 rows each of 8 experts, 4096 x 14336: 82 us, 64 x 64 88 us; 16 x 4096 x 14336 (56 items): 24 and 11 us
-  if (avg <= 32 && 4 * items(32, 256) >= 5 * cus) return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, 1, s);
+  if (avg > 32 && 4 * items(64, 128) >= 3 * cus) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, s);
+  // Few rows, two workgroups a CU, where the rounds are at least three
+  // quarters full: 16 rows each of 8 experts, 4096 x 14336 (448 items) 82 us,
+  // 64 x 64 88 us; 7 rows each of 64 experts, 1776 x 2464 (640): 75 and 62 us;
+  // 16 x 4096 x 14336 (56): 24 and 11 us
+  const long long n32 = items(32, 256), round = 2 * cus;
+  if (avg <= 32 && 3 * ((n32 + round - 1) / round * round) <= 4 * n32) return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, 1, s);
   // 64 x 4096 x 14336: 12 us, 32 rows on private rings 22 us
-  if ((avg > 16 || a.E > 1) && items(64, 64) >= enough) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, 0, s);
+  if ((avg > 16 || a.E > 1) && 4 * items(64, 64) >= 3 * cus) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, 0, s);
   // 16 x 14336 x 4096 (64 items of 64 channels): 11.4 us, 64 x 64 29 us
   if (avg <= 16) return launch_rows<1, 2, 4, 2>(a, y_bf16, s);
   // 64 x 14336 x 4096: 13.7 us, 64 x 64 29.5 us
