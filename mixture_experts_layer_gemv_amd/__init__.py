@@ -116,6 +116,18 @@ def lib():
     return _lib
 
 
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
 def _p(t):
     if t is None:
         return None
@@ -126,8 +138,7 @@ def _p(t):
 
 def _s(stream):
     if stream is None:
-        import torch
-
+        torch = _torch()
         # torch.cuda.current_stream().cuda_stream without building a Stream object
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
@@ -234,11 +245,10 @@ def _tensors(fn, *sized):
     out, dev = [], -1
     for t, nbytes in sized:
         if t is not None and type(t) is not int:
-            if dev < 0 and t.is_cuda:
-                import torch
-
-                dev = torch.cuda.current_device()
-            if not t.is_cuda or t.get_device() != dev or t.nbytes < nbytes or not t.is_contiguous():
+            d = t.get_device()  # -1: not on a GPU
+            if dev < 0 <= d:
+                dev = _torch().cuda.current_device()
+            if d < 0 or d != dev or t.nbytes < nbytes or not t.is_contiguous():
                 raise MoeError(fn, MOE_ERR_INVALID_ARG, f"tensor {tuple(t.shape)} on {t.device}: need {nbytes} "
                                "contiguous bytes on the current GPU")
             t = t.data_ptr()
