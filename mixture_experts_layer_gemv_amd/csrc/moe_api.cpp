@@ -18,6 +18,7 @@
 #include "moe_index.hpp"
 #include "moe_kernels.hpp"
 #include "moe_rows.hpp"
+#include "moe_rows_index.hpp"
 
 // The plan inputs of a layer: its shape, dtypes and tuning.  Every launch
 // choice and the workspace layout are functions of this, T and k (and the
@@ -1631,7 +1632,7 @@ moe_status check_norm(int dtype, int norm, int T, int m) {
 }
 
 size_t norm_backward_bytes(int T, int m) {
-  return (size_t)2 * (size_t)moe::norm_backward_blocks(T, m, device_cus()) * (size_t)m * sizeof(float);
+  return (size_t)2 * (size_t)moe::norm_bwd_blocks(T, m, device_cus()) * (size_t)m * sizeof(float);
 }
 
 // Shapes of the permute and combine operators.

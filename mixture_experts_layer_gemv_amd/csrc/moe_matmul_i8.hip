@@ -11,10 +11,10 @@
 // token.
 #include <type_traits>
 
-#include "moe_index.hpp"
 #include "moe_kernels.hpp"
 #include "moe_lds.hpp"
 #include "moe_rows.hpp"
+#include "moe_rows_index.hpp"
 
 namespace moe {
 namespace {
@@ -96,15 +96,6 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
-// A 128-byte line of a row r in LDS: its chunk c of 16 bytes is stored at place
-// c ^ ((r >> 1) & 7).  Products read the same chunk of 16 successive rows in
-// one LDS cycle (256 bytes): even rows lie in the lower and odd rows in the
-// upper half of the banks, and the 8 rows of each half at 8 places, so no bank
-// is read twice (r & 7 in its place: half of the LDS cycles were conflicts).
-// The copy of lines 8 i .. 8 i + 7 makes that order by the chunk that each lane
-// fetches: lane l writes place l % 8 of line 8 i + l / 8.
-__device__ __forceinline__ int chunk_of(int i, int lane) { return (lane & 7) ^ ((4 * i + (lane >> 4)) & 7); }
-
 // global -> LDS, 16 bytes a lane from 64-bit addresses (see copy_frag).
 __device__ __forceinline__ void copy_rows(const void* p, uint32_t lds) {
   uint32_t saved;
@@ -168,7 +159,7 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
       copy_rows(xsrc[j] + min(k0 + 16 * chunk_of(j, lane), A.K - 16), at + j * 1024);
   };
   i32x4_t acc[CB][TB] = {};
-  const int rowoff = (lane & 15) * 128, quart = lane >> 4;
+  const int quart = lane >> 4;
   if (lo < hi) {
 #pragma unroll
     for (int s = 0; s < S; ++s) issue(lo + s, s);
@@ -179,7 +170,7 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
       i32x4_t wv[2][CB], xv[2][TB];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const int at = rowoff + (((4 * ks + quart) ^ ((lane >> 1) & 7)) * 16);
+        const int at = operand16(lane, ks);
 #pragma unroll
         for (int c = 0; c < CB; ++c) wv[ks][c] = *reinterpret_cast<const i32x4_t*>(st + (CPX + 2 * c) * 1024 + at);
 #pragma unroll
@@ -248,7 +239,7 @@ hipError_t launch_rows(const I8Args& a, bool y_bf16, hipStream_t s) {
 // A workgroup of WT x WC waves computes 32 TB WT rows by 32 CB WC channels of
 // one expert.  A stage is 128 bytes of the reduction: one cache line of every
 // row and channel of the tile, copied into LDS with 16 bytes a lane, eight
-// lines a copy, S stages in a ring (see chunk_of for a line's order in LDS).
+// lines a copy, S stages in a ring (see line_place for a line's order in LDS).
 //
 // What bounds it: large products (256 x 256 tiles, two waves per SIMD, 128 x
 // 64 each) the power of products, LDS reads and copies together.  8192 x 4096
@@ -257,16 +248,6 @@ hipError_t launch_rows(const I8Args& a, bool y_bf16, hipStream_t s) {
 // A deeper ring (96 KiB under way instead of 64) and four waves of 128 x 128
 // (a third fewer LDS reads) measured 2 and 3 % slower.  Products of few rows
 // (32 x 256 tiles) stream their weights at 5.6 TB/s.
-template <int TB, int CB, int WT, int WC, int S>
-struct TileShape {
-  static constexpr int waves = WT * WC;
-  static constexpr int BM = 32 * TB * WT, BN = 32 * CB * WC;
-  static constexpr int XB = BM * 128, WB = BN * 128;  // bytes of a stage
-  static constexpr int CPX = BM / 8 / waves, CPW = BN / 8 / waves, CP = CPX + CPW;  // copies per wave and stage
-  static_assert(BM % (8 * waves) == 0 && BN % (8 * waves) == 0, "every wave issues the same copies");
-  static_assert(CP * (S - 1) <= 63, "vmcnt holds at most 63");
-};
-
 template <int TB, int CB, int WT, int WC, int S, bool YB>
 __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg,
                                                                                                      int rotate) {
@@ -327,9 +308,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[c][i][v] = 0;
 
-  // operand reads: lane l takes chunk 2 ks + l / 32 of row l % 32 of a block
   const int half = lane >> 5;
-  const int rowoff = (lane & 31) * 128;
   struct Frag {
     i32x4_t x[TB], w[CB];
   };
@@ -344,7 +323,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
     // operand j of quarter ks of stage s: the channel blocks, then the row blocks
     auto load_one = [&](Frag& f, int s, int ks, int j) {
       const unsigned char* st = ring[s % S];
-      const int at = rowoff + (((2 * ks + half) ^ ((lane >> 1) & 7)) * 16);
+      const int at = operand32(lane, ks);
       if (j < CB) f.w[j] = *reinterpret_cast<const i32x4_t*>(st + Sh::XB + (wc * CB + j) * 4096 + at);
       else f.x[j - CB] = *reinterpret_cast<const i32x4_t*>(st + (wt * TB + j - CB) * 4096 + at);
     };
@@ -414,13 +393,12 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   else reduce(std::integral_constant<int, 1>{});
   __syncthreads();  // the ring is free
 
-  // Epilogue: element v of acc[c][i] in lane l is channel 8 (v / 4) + 4 (l /
-  // 32) + v % 4 of channel block c and row l % 32 of row block i.  A wave
+  // Epilogue: element v of acc[c][i] in lane l is channel acc_channel(l, v) of
+  // channel block c and row l % 32 of row block i.  A wave
   // stages one row block at a time (32 rows by its 32 CB channels, rows padded
   // by 16 bytes) and stores it 16 bytes a lane, whole lines of a row together.
   constexpr int ES = YB ? 2 : 4;
-  constexpr int RB = 32 * CB * ES, STR = RB + 16;  // bytes of a staged row, its stride
-  static_assert(WT * WC * 32 * STR <= S * (Sh::XB + Sh::WB), "the staging fits the ring");
+  constexpr int RB = Sh::row_bytes(ES), STR = Sh::stride(ES);
   unsigned char* const stage = &ring[0][0] + wave * 32 * STR;
   const int nw = n0 + wc * 32 * CB;  // the wave's first channel
   float sw[CB][16];

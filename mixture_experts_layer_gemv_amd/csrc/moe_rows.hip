@@ -11,6 +11,7 @@
 // combine's gradient 66.3 us (5.1).
 #include "moe_kernels.hpp"
 #include "moe_rows.hpp"
+#include "moe_rows_index.hpp"
 
 namespace moe {
 namespace {
@@ -110,18 +111,9 @@ __device__ __forceinline__ float group_sum(float v, int n) {
 // ---- norm -----------------------------------------------------------------------
 //
 // A team of NT threads (8, 16, 32 or a multiple of 64) owns a row; a block
-// holds one or more teams.  A thread keeps V times eight elements: eight
-// together for bf16, twice four for fp32, so that a wave's 16-byte loads and
-// stores always cover whole lines.
+// holds one or more teams.  A thread keeps V times eight elements (norm_cols).
 template <bool BF16>
-struct Cols {
-  int lo, hi;  // the first columns of the two fours
-  __device__ __forceinline__ Cols(int tid, int NT, int v)
-      : lo(BF16 ? 8 * (tid + v * NT) : 4 * (tid + 2 * v * NT)), hi(BF16 ? lo + 4 : lo + 4 * NT) {}
-};
-
-template <bool BF16>
-__device__ __forceinline__ void load_raw(u32x4_t (&v)[BF16 ? 1 : 2], const void* p, size_t row, Cols<BF16> c, int m) {
+__device__ __forceinline__ void load_raw(u32x4_t (&v)[BF16 ? 1 : 2], const void* p, size_t row, NormCols c, int m) {
 #pragma unroll
   for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
     const int at = i ? c.hi : c.lo;
@@ -145,7 +137,7 @@ __device__ __forceinline__ void from_raw(const u32x4_t (&v)[BF16 ? 1 : 2], float
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store_row(void* p, size_t row, Cols<BF16> c, int m, const float (&f)[8]) {
+__device__ __forceinline__ void store_row(void* p, size_t row, NormCols c, int m, const float (&f)[8]) {
   if constexpr (BF16) {
     if (c.lo < m) store8<true>(p, row + c.lo, f);
   } else {
@@ -156,7 +148,7 @@ __device__ __forceinline__ void store_row(void* p, size_t row, Cols<BF16> c, int
 
 // The same columns of an fp32 vector (gamma, beta, a row of partial sums); 0 past m.
 template <bool BF16>
-__device__ __forceinline__ void load_vec(const float* p, Cols<BF16> c, int m, float (&f)[8]) {
+__device__ __forceinline__ void load_vec(const float* p, NormCols c, int m, float (&f)[8]) {
   const f32x4_t zero = {0, 0, 0, 0};
   const f32x4_t a = c.lo < m ? *reinterpret_cast<const f32x4_t*>(p + c.lo) : zero;
   const f32x4_t b = c.hi < m ? *reinterpret_cast<const f32x4_t*>(p + c.hi) : zero;
@@ -168,7 +160,7 @@ __device__ __forceinline__ void load_vec(const float* p, Cols<BF16> c, int m, fl
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store_vec(float* p, Cols<BF16> c, int m, const float (&f)[8]) {
+__device__ __forceinline__ void store_vec(float* p, NormCols c, int m, const float (&f)[8]) {
   if (c.lo < m) *reinterpret_cast<f32x4_t*>(p + c.lo) = f32x4_t{f[0], f[1], f[2], f[3]};
   if (c.hi < m) *reinterpret_cast<f32x4_t*>(p + c.hi) = f32x4_t{f[4], f[5], f[6], f[7]};
 }
@@ -200,7 +192,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
   float g[V][8], b[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const Cols<BF16> c(tid, NT, v);
+    const NormCols c = norm_cols(BF16, tid, NT, v);
     load_vec<BF16>(A.gamma, c, m, g[v]);
     if (LAYER && A.beta) load_vec<BF16>(A.beta, c, m, b[v]);
     else
@@ -211,7 +203,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
   auto fetch = [&](long long t) {
     if (t >= A.T) t = A.T - 1;  // read, never written
 #pragma unroll
-    for (int v = 0; v < V; ++v) load_raw<BF16>(next[v], A.x, (size_t)t * m, Cols<BF16>(tid, NT, v), m);
+    for (int v = 0; v < V; ++v) load_raw<BF16>(next[v], A.x, (size_t)t * m, norm_cols(BF16, tid, NT, v), m);
   };
   const long long stride = (long long)gridDim.x * teams;
   fetch((long long)blockIdx.x * teams + team);
@@ -234,7 +226,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
     float q = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Cols<BF16> c(tid, NT, v);
+      const NormCols c = norm_cols(BF16, tid, NT, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = (j < 4 ? c.lo : c.hi) < m ? f[v][j] - mu : 0.0f;
@@ -254,7 +246,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = LAYER ? fmaf(f[v][j] * r, g[v][j], b[v][j]) : f[v][j] * r * g[v][j];
-      store_row<BF16>(A.out, (size_t)t * m, Cols<BF16>(tid, NT, v), m, o);
+      store_row<BF16>(A.out, (size_t)t * m, norm_cols(BF16, tid, NT, v), m, o);
     }
   }
 }
@@ -276,7 +268,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
   float g[V][8], ag[V][8], ab[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    load_vec<BF16>(A.gamma, Cols<BF16>(tid, NT, v), m, g[v]);
+    load_vec<BF16>(A.gamma, norm_cols(BF16, tid, NT, v), m, g[v]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) ag[v][j] = ab[v][j] = 0.0f;
   }
@@ -286,7 +278,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
     const long long row = t < A.T ? t : A.T - 1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Cols<BF16> c(tid, NT, v);
+      const NormCols c = norm_cols(BF16, tid, NT, v);
       load_raw<BF16>(nx[v], A.x, (size_t)row * m, c, m);
       load_raw<BF16>(ny[v], A.dy, (size_t)row * m, c, m);
     }
@@ -312,7 +304,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
     if (AHEAD && t0 + stride < A.T) fetch(t + stride);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Cols<BF16> c(tid, NT, v);
+      const NormCols c = norm_cols(BF16, tid, NT, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // outside the row x and dy are 0: h would be -mu r, times 0; kept finite
@@ -356,7 +348,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (LAYER ? u[v][j] - m2 - h[v][j] * m1 : u[v][j] - h[v][j] * m1) * r;
-      store_row<BF16>(A.out, (size_t)t * m, Cols<BF16>(tid, NT, v), m, o);
+      store_row<BF16>(A.out, (size_t)t * m, norm_cols(BF16, tid, NT, v), m, o);
     }
   }
   if (!A.partial) return;
@@ -375,7 +367,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
     if (group == k && owner)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Cols<BF16> c(tid, NT, v);
+        const NormCols c = norm_cols(BF16, tid, NT, v);
         store_vec<BF16>(acc, c, m, ag[v]);
         if (LAYER) store_vec<BF16>(acc + m, c, m, ab[v]);
       }
@@ -383,7 +375,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
     if (group == 0 && owner)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Cols<BF16> c(tid, NT, v);
+        const NormCols c = norm_cols(BF16, tid, NT, v);
         float f[8];
         load_vec<BF16>(acc, c, m, f);
 #pragma unroll
@@ -402,7 +394,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
   float* const pb = one ? A.dbeta : A.partial + (size_t)(gridDim.x + blockIdx.x) * m;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const Cols<BF16> c(tid, NT, v);
+    const NormCols c = norm_cols(BF16, tid, NT, v);
     if (pg) store_vec<BF16>(pg, c, m, ag[v]);
     if (LAYER && pb) store_vec<BF16>(pb, c, m, ab[v]);
   }
@@ -575,16 +567,6 @@ unsigned wave_grid(long long items) {  // four waves a block, an item each
   return blocks < kMaxGrid ? (unsigned)blocks : (unsigned)kMaxGrid;
 }
 
-// Threads of a team for rows of m with V vectors of 8 per thread.
-int norm_threads(int m, int V) {
-  const int n = (m + 8 * V - 1) / (8 * V);
-  return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : (n + 63) / 64 * 64;
-}
-int norm_vecs(int m) { return m <= 8192 ? 1 : 2; }
-// Teams of a block.
-int norm_fwd_teams(int nt) { return nt <= 256 ? 256 / nt : 1; }
-int norm_bwd_teams(int nt) { return nt <= 512 ? 512 / nt : 1; }
-
 }  // namespace
 
 #define MOE_NORM(KERNEL, ...)                               \
@@ -598,7 +580,7 @@ int norm_bwd_teams(int nt) { return nt <= 512 ? 512 / nt : 1; }
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
-  const int V = norm_vecs(a.m), nt = norm_threads(a.m, V), teams = norm_fwd_teams(nt), threads = nt * teams;
+  const int V = norm_vecs(a.m), nt = norm_threads(a.m), teams = norm_fwd_teams(nt), threads = nt * teams;
   const long long blocks = ((long long)a.T + teams - 1) / teams, most = (long long)cus * (V == 1 ? 2048 / threads : 1);
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
 #define MOE_FWD1(B, L) k_norm_fwd<B, 1, L>
@@ -610,25 +592,11 @@ hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus
   return hipGetLastError();
 }
 
-// So few steps that one block takes them all and no second launch is needed
-// (rows of 4096: 4 steps 6.3 us, against 8.7 us for 5 on 5 blocks; 8192: 7.6
-// us).  Rows past 8192 columns, without the next row loaded ahead, take 11 us.
-constexpr int kOneBlockSteps = 4;
-
-int norm_backward_blocks(int T, int m, int cus) {
-  const int nt = norm_threads(m, norm_vecs(m)), teams = norm_bwd_teams(nt);
-  const long long steps = ((long long)T + teams - 1) / teams, most = (long long)cus * (nt < 256 ? 2 : 1);
-  if (steps <= kOneBlockSteps && norm_vecs(m) == 1) return steps > 0;
-  if (steps <= most) return (int)steps;
-  const long long per = (steps + most - 1) / most;  // the same number of steps for every block but the last
-  return (int)((steps + per - 1) / per);
-}
-
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
-  const int V = norm_vecs(a.m), nt = norm_threads(a.m, V), threads = nt * norm_bwd_teams(nt);
-  const unsigned grid = (unsigned)norm_backward_blocks(a.T, a.m, cus);
+  const int V = norm_vecs(a.m), nt = norm_threads(a.m), threads = nt * norm_bwd_teams(nt);
+  const unsigned grid = (unsigned)norm_bwd_blocks(a.T, a.m, cus);
   const size_t lds = threads > (nt < 64 ? 64 : nt) ? 2 * sizeof(float) * (size_t)a.m : 0;  // at most 2048 columns
 #define MOE_BWD1(B, L) k_norm_bwd<B, 1, L>
 #define MOE_BWD2(B, L) k_norm_bwd<B, 2, L>

@@ -11,9 +11,6 @@
 
 namespace moe {
 
-// Widest row of the norm operators: 1024 threads with two 8-element vectors.
-constexpr int kNormMaxCols = 16384;
-
 struct NormArgs {
   const void* x;       // [T][m] bf16 or fp32
   const void* dy;      // backward: [T][m] in x's dtype
@@ -30,8 +27,6 @@ struct NormArgs {
 };
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s);
-// Rows of partial sums (per gradient) a backward pass over T rows of m writes.
-int norm_backward_blocks(int T, int m, int cus);
 
 struct RowsArgs {
   const void* tok;     // token rows [T][m]: x (permute), dy (combine's gradient)
