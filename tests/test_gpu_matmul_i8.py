@@ -228,6 +228,17 @@ def test_offsets_past_32_bits():
     y = run(x, sx, w, sw, offsets, perm, 1, rows, BF16)
     check(y, exact(x, sx, w, sw, offsets, perm, 1, rows), BF16)
     del w, y
+    K, N, T = 4096, 264, 1_100_000  # 4.5 GB of tokens, a few of them used
+    x = torch.zeros(T, K, dtype=torch.int8, device="cuda")
+    use = torch.tensor([0, 1, 524_287, 524_288, 1_048_575, 1_048_576, T - 2, T - 1], device="cuda")
+    x[use] = codes((len(use), K), 9)
+    w, sx, sw = codes((2, N, K), 10), scales((T,), 11), scales((2, N), 12)
+    for rows in (8, 400):  # few rows, and a tile
+        perm = use.repeat((rows + 7) // 8)[:rows].to(torch.int32)
+        offsets = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device="cuda")
+        y = run(x, sx, w, sw, offsets, perm, 1, rows, F32)
+        check(y, exact(x, sx, w, sw, offsets, perm, 1, rows), F32)
+    del x, w, y
     K, N, R = 64, 32768, 70000  # 2.3e9 outputs
     x, w, sx, sw = codes((R, K), 1), codes((1, N, K), 2), scales((R,), 3), scales((1, N), 4)
     y = torch.empty(R, N, dtype=BF16, device="cuda")

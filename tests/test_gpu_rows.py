@@ -189,6 +189,21 @@ def test_norm_backward(T, m, layer, dtype):
         assert torch.equal(one, db.t)
 
 
+def test_norm_without_eps_and_unaligned_refused():
+    """eps 0 on rows that vary; a pointer off its 16 bytes is refused, not read."""
+    T, m = 3, 264
+    x, g = rnd((T, m), F32, 1, 3.0), rnd((m,), F32, 2, 0.1, 1.0)
+    y = torch.empty_like(x)
+    M.moe_norm_forward(x, M.MOE_F32, M.MOE_NORM_RMS, g, None, 0.0, T, m, y)
+    ref = norm_ref(n64(x), n64(g), None, 0.0, False)[0]
+    assert np.all(np.abs(n64(y) - ref) <= (m + 20) * u * np.abs(ref))
+    off = torch.empty(T * m + 1, device="cuda")[1:].view(T, m)
+    for args in [(off, g, None, y), (x, g, None, off)]:
+        with pytest.raises(M.MoeError) as ei:
+            M.moe_norm_forward(args[0], M.MOE_F32, M.MOE_NORM_RMS, args[1], args[2], 0.0, T, m, args[3])
+        assert ei.value.status == M.MOE_ERR_INVALID_ARG
+
+
 def test_norm_backward_of_no_rows():
     dg, db = torch.full((136,), 3.0, device="cuda"), torch.full((136,), 3.0, device="cuda")
     M.moe_norm_backward(None, None, M.MOE_F32, M.MOE_NORM_LAYER, None, None, None, 0, 128, None, dg[:128], db[:128])
