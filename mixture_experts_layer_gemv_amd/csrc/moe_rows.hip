@@ -505,7 +505,8 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
   __shared__ float dots[4][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, NT = blockDim.x, waves = NT >> 6;
   const int mv = A.m / 8;
-  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
+  for (long long i = blockIdx.x; i < A.T; i += gridDim.x) {  // the step past the last token may pass 2^31
+    const int t = (int)i;
     const int mine = token_rows(A, t, lane);
     const float wl = lane < A.k && A.w ? A.w[(size_t)t * A.k + lane] : 0.0f;
     dots[wave][lane] = 0.0f;

@@ -428,3 +428,38 @@ def test_offsets_past_32_bits():
     dx = torch.empty_like(xx)
     M.moe_norm_backward(y, xx, M.MOE_BF16, M.MOE_NORM_RMS, g, None, rstd, len(xx), m, dx, None, None)
     assert torch.equal(dx[T:], dx[:T])
+
+
+def test_as_many_tokens_as_an_int_counts():
+    """T = 2^31 - 8 with k = 1: no loop over tokens may step past the last one
+    in 32 bits.  Four tokens have a row; the products are exact."""
+    T, m, rows = 2**31 - 8, 8, 4
+    if torch.cuda.mem_get_info()[0] < 70 << 30:
+        pytest.skip("needs 70 GB")
+    toks = torch.tensor([0, 2**22, 2**31 - 2**22, T - 1], device="cuda")
+    inv = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    inv[toks] = torch.arange(rows, dtype=torch.int32, device="cuda")
+    x = torch.full((T, m), 2.0, dtype=BF16, device="cuda")
+    x[toks] = torch.tensor([1.0, 3.0, 5.0, 7.0], dtype=BF16, device="cuda")[:, None]
+    yp = torch.full((rows, m), 0.5, dtype=BF16, device="cuda")
+    w = torch.full((T,), 4.0, dtype=F32, device="cuda")
+
+    xp = torch.zeros((rows, m), dtype=BF16, device="cuda")
+    M.moe_permute_rows(x, M.MOE_BF16, inv, T, m, 1, rows, xp)
+    assert xp[:, 0].tolist() == [1.0, 3.0, 5.0, 7.0] and bool((xp == xp[:, :1]).all())
+
+    dyp = torch.zeros_like(yp)
+    dw = torch.full((T,), 9.0, dtype=F32, device="cuda")
+    M.moe_combine_rows_backward(x, M.MOE_BF16, yp, M.MOE_BF16, inv, w, T, m, 1, rows, dyp, dw)
+    assert dyp[:, 0].tolist() == [4.0, 12.0, 20.0, 28.0] and bool((dyp == dyp[:, :1]).all())
+    assert dw[toks].tolist() == [4.0, 12.0, 20.0, 28.0]
+    dw[toks] = 0.0
+    assert float(dw.abs().amax()) == 0.0
+    del dw
+
+    M.moe_combine_rows(yp, M.MOE_BF16, inv, w, T, m, 1, rows, x, M.MOE_BF16)
+    assert bool((x[toks] == 2.0).all())
+    x[toks] = 0.0
+    assert float(x.amax()) == 0.0 and float(x.amin()) == 0.0
+    del x, inv, w
+    torch.cuda.empty_cache()
