@@ -241,16 +241,17 @@ def moe_quantize_rows_i8(x, T, m, xq, scale, stream=None):
 def _tensors(fn, *sized):
     """The row operators' tensor arguments as device pointers, each given with
     the bytes the call reads or writes there; a tensor that is not on the
-    current GPU, not contiguous or too small raises before the call."""
+    current GPU, not contiguous, too small or of 64-bit elements (torch's own
+    indices: the calls take int32) raises before the call."""
     out, dev = [], -1
     for t, nbytes in sized:
         if t is not None and type(t) is not int:
             d = t.get_device()  # -1: not on a GPU
             if dev < 0 <= d:
                 dev = _torch().cuda.current_device()
-            if d < 0 or d != dev or t.nbytes < nbytes or not t.is_contiguous():
-                raise MoeError(fn, MOE_ERR_INVALID_ARG, f"tensor {tuple(t.shape)} on {t.device}: need {nbytes} "
-                               "contiguous bytes on the current GPU")
+            if d < 0 or d != dev or t.nbytes < nbytes or t.itemsize > 4 or not t.is_contiguous():
+                raise MoeError(fn, MOE_ERR_INVALID_ARG, f"{t.dtype} tensor {tuple(t.shape)} on {t.device}: need "
+                               f"{nbytes} contiguous bytes of at most 32-bit elements on the current GPU")
             t = t.data_ptr()
         out.append(t)
     return out

@@ -298,3 +298,26 @@ def test_binding_refuses_small_and_strided_tensors():
         with pytest.raises(M.MoeError) as ei:
             M.moe_norm_forward(bad[0], M.MOE_F32, M.MOE_NORM_RMS, bad[1], None, 1e-5, 8, 64, bad[2])
         assert ei.value.status == M.MOE_ERR_INVALID_ARG
+
+
+def test_binding_refuses_64_bit_indices():
+    """torch's own index type, whose halves would be read as int32."""
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.full((4, 2), 0.5, device="cuda")
+    inv = torch.randperm(8, device="cuda")  # int64
+    rows = torch.empty(8, 64, dtype=torch.bfloat16, device="cuda")
+    B = M.MOE_BF16
+    q, s = torch.ones(8, 64, dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    y = torch.empty(8, 64, device="cuda")
+    off = torch.tensor([0, 8], device="cuda")
+    calls = [lambda i: M.moe_permute_rows(x, B, i, 4, 64, 2, 8, rows),
+             lambda i: M.moe_permute_rows_backward(rows, B, i, 4, 64, 2, 8, x, B),
+             lambda i: M.moe_combine_rows(rows, B, i, w, 4, 64, 2, 8, x, B),
+             lambda i: M.moe_combine_rows_backward(x, B, rows, B, i, w, 4, 64, 2, 8, torch.empty_like(rows), None),
+             lambda i: M.moe_matmul_i8(q, s, q, s, off if i.dtype == torch.int64 else off.int(), i, 8, 1, 8, 64, 8, 1,
+                                       y, M.MOE_F32)]
+    for call in calls:
+        with pytest.raises(M.MoeError) as ei:
+            call(inv)
+        assert ei.value.status == M.MOE_ERR_INVALID_ARG and "int64" in ei.value.message
+        call(inv.int())
