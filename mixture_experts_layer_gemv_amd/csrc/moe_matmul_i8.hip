@@ -27,6 +27,7 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 // One (expert, row block, column block) of a launch.
 struct Item {
   int e, mb, nb;   // e < 0: none
+  int blocks;      // row blocks of the expert
   int row0, rows;  // the block's first row and its rows
 };
 
@@ -37,7 +38,7 @@ struct Item {
 // caller's array holds.  spread: L is the block's number, dealt evenly over
 // the XCDs (xcd_item); else it is the item.
 __device__ __forceinline__ Item find_item(const I8Args& A, int BM, int NBL, int cg, int L, bool spread) {
-  Item it{-1, 0, 0, 0, 0};
+  Item it{-1, 0, 0, 0, 0, 0};
   int e = 0, lo = 0, hi = A.R, before = 0;  // the item's expert, its rows, the items before it
   if (!A.offsets) {
     const int total = (hi + BM - 1) / BM * NBL;
@@ -80,6 +81,7 @@ __device__ __forceinline__ Item find_item(const I8Args& A, int BM, int NBL, int 
     it.nb = li - it.mb * NBL;
   }
   it.e = e;
+  it.blocks = blocks;
   it.row0 = lo + it.mb * BM;
   it.rows = min(BM, hi - it.row0);
   return it;
@@ -109,9 +111,31 @@ __device__ __forceinline__ void copy_rows(const void* p, uint32_t lds) {
       : "memory");
 }
 
+// copy_frag of a weight line that nothing reads again.
+__device__ __forceinline__ void copy_once(const void* sbase, uint32_t voff, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "global_load_lds_dwordx4 %1, %2 nt\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(voff), "s"(sbase), "s"(lds)
+      : "memory");
+}
+
 // Upper bound on the row blocks of BM rows.
 long long row_blocks(const I8Args& a, int BM) {
   return a.offsets ? (long long)a.R / BM + (a.R < a.E ? a.R : a.E) : ((long long)a.R + BM - 1) / BM;
+}
+
+// go(y_bf16, nt), both known to the compiler.
+template <class F>
+void dispatch(F go, bool y_bf16, bool nt) {
+  const std::true_type yes{};
+  const std::false_type no{};
+  if (y_bf16) nt ? go(yes, yes) : go(yes, no);
+  else nt ? go(no, yes) : go(no, no);
 }
 
 // ---- few rows: every wave streams weights of its own -----------------------------
@@ -120,10 +144,13 @@ long long row_blocks(const I8Args& a, int BM) {
 // its W waves split the reduction and add their int32 sums in LDS.  Each wave
 // copies its own lines through a private ring of S stages (128 bytes of every
 // row and channel), so no wave waits for another before the final sum.  The
-// weights' bytes bound it: 16 x 4096 x 14336 takes 11.1 us, 5.3 TB/s (a large
-// copy reaches 5.0 on this card).  Weights loaded straight into registers,
-// half a line an instruction, took 13.5 us.
-template <int TB, int CB, int W, int S, bool YB>
+// weights' bytes bound it: 16 x 14336 x 4096 takes 11.3 us, 5.2 TB/s, and 16 x
+// 28672 x 8192 37 us, 6.3 TB/s (a large copy reaches 5.0 on this card).  Weights
+// loaded straight into registers, half a line an instruction, took 13.5 us
+// where these copies took 11.1 (16 x 4096 x 14336).  Neighbouring workgroups
+// start from different stages, see k_i8_tile (16 x 16384 x 8192: 31 against 24 us).
+// NT: weights that only one row block of the expert reads are not kept.
+template <int TB, int CB, int W, int S, bool YB, bool NT>
 __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   constexpr int CPX = 2 * TB, CPW = 2 * CB, CP = CPX + CPW;
   static_assert(CP * S <= 63, "vmcnt holds at most 63");
@@ -148,21 +175,26 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   const uint32_t at0 = lds_address(ring);
   const int steps = (A.K + 127) / 128;
   const int lo = (int)((long long)steps * wave / W), hi = (int)((long long)steps * (wave + 1) / W);
-  auto issue = [&](int s, int slot) {
-    const int k0 = min(s, hi - 1) * 128;  // past K: any bytes of the row, multiplied by zeros
+  const int rot = lo < hi ? it.nb % (hi - lo) : 0;
+  auto stage_of = [&](int s) { return s + rot < hi ? s + rot : s + rot - (hi - lo); };
+  auto issue = [&](int s, int slot, auto once) {
+    const int k0 = stage_of(min(s, hi - 1)) * 128;  // past K: any bytes of the row, multiplied by zeros
     const uint32_t at = at0 + (uint32_t)slot * STAGE;
 #pragma unroll
-    for (int j = 0; j < CPW; ++j)
-      copy_frag(wbase, wsrc[j] + (uint32_t)min(k0 + 16 * chunk_of(j, lane), A.K - 16), at + (CPX + j) * 1024);
+    for (int j = 0; j < CPW; ++j) {
+      const uint32_t from = wsrc[j] + (uint32_t)min(k0 + 16 * chunk_of(j, lane), A.K - 16);
+      if constexpr (decltype(once)::value) copy_once(wbase, from, at + (CPX + j) * 1024);
+      else copy_frag(wbase, from, at + (CPX + j) * 1024);
+    }
 #pragma unroll
     for (int j = 0; j < CPX; ++j)
       copy_rows(xsrc[j] + min(k0 + 16 * chunk_of(j, lane), A.K - 16), at + j * 1024);
   };
   i32x4_t acc[CB][TB] = {};
   const int quart = lane >> 4;
-  if (lo < hi) {
+  auto reduce = [&](auto once) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) issue(lo + s, s);
+    for (int s = 0; s < S; ++s) issue(lo + s, s, once);
     int slot = 0;
     for (int s = lo; s < hi; ++s) {
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(CP * (S - 1)) : "memory");
@@ -176,15 +208,15 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
 #pragma unroll
         for (int i = 0; i < TB; ++i) xv[ks][i] = *reinterpret_cast<const i32x4_t*>(st + 2 * i * 1024 + at);
       }
-      if ((s + 1) * 128 > A.K) {  // the tail: zero weights past K
+      if ((stage_of(s) + 1) * 128 > A.K) {  // the tail: zero weights past K
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int c = 0; c < CB; ++c)
-            if (s * 128 + 64 * ks + 16 * quart >= A.K) wv[ks][c] = i32x4_t{0, 0, 0, 0};
+            if (stage_of(s) * 128 + 64 * ks + 16 * quart >= A.K) wv[ks][c] = i32x4_t{0, 0, 0, 0};
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
-      issue(s + S, slot);
+      issue(s + S, slot, once);
       slot = slot + 1 == S ? 0 : slot + 1;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
@@ -195,6 +227,10 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
             acc[c][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[ks][c], xv[ks][i], acc[c][i], 0, 0, 0);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the last copies have landed: the ring is reused
+  };
+  if (lo < hi) {
+    if (NT && it.blocks == 1) reduce(std::integral_constant<bool, NT>{});
+    else reduce(std::false_type{});
   }
   __syncthreads();
   i32x4_t* const part = reinterpret_cast<i32x4_t*>(lds);  // [W][CB * TB][64]
@@ -225,12 +261,15 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
 }
 
 template <int TB, int CB, int W, int S>
-hipError_t launch_rows(const I8Args& a, bool y_bf16, hipStream_t s) {
+hipError_t launch_rows(const I8Args& a, bool y_bf16, bool large, hipStream_t s) {
   const long long cols = (a.N + 16 * CB - 1) / (16 * CB);
   const long long blocks = row_blocks(a, 16 * TB) * cols;
   if (blocks * W * 64 >= 1LL << 32) return hipErrorInvalidValue;
-  if (y_bf16) k_i8_rows<TB, CB, W, S, true><<<(unsigned)blocks, W * 64, 0, s>>>(a, (int)cols);
-  else k_i8_rows<TB, CB, W, S, false><<<(unsigned)blocks, W * 64, 0, s>>>(a, (int)cols);
+  auto go = [&](auto yb, auto nt) {
+    constexpr bool YB = decltype(yb)::value, NT = decltype(nt)::value;
+    k_i8_rows<TB, CB, W, S, YB, NT><<<(unsigned)blocks, W * 64, 0, s>>>(a, (int)cols);
+  };
+  dispatch(go, y_bf16, large);
   return hipGetLastError();
 }
 
@@ -247,10 +286,11 @@ hipError_t launch_rows(const I8Args& a, bool y_bf16, hipStream_t s) {
 // LDS reads 350 us, the copies alone 290 us, while the clock falls to 1.8 GHz.
 // A deeper ring (96 KiB under way instead of 64) and four waves of 128 x 128
 // (a third fewer LDS reads) measured 2 and 3 % slower.  Products of few rows
-// (32 x 256 tiles) stream their weights at 5.6 TB/s.
-template <int TB, int CB, int WT, int WC, int S, bool YB>
+// (32 x 256 tiles) stream their weights at 6.5 TB/s.  NT: an expert's weights
+// that only one row block reads are not kept.
+template <int TB, int CB, int WT, int WC, int S, bool YB, bool NT>
 __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg,
-                                                                                                     int rotate) {
+                                                                                                     bool rotate) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   __shared__ __attribute__((aligned(1024))) unsigned char ring[S][Sh::XB + Sh::WB];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -280,11 +320,12 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   // Where a weight tile is read once (rotate), neighbouring column blocks walk
   // the reduction from different stages: in step with one another they read
   // the same offset of rows a power of two apart, few of the memory's channels
-  // (474 MB of decode weights: 100 against 84 us).  A partial stage stays the last.
+  // (16 rows each of 8 experts, 470 MB of weights: 84 against 72 us).  A partial stage
+  // stays the last.
   const int full = A.K / 128, rot = rotate && full ? it.nb % full : 0;
   auto stage_of = [&](int s) { return s >= full ? s : (s + rot < full ? s + rot : s + rot - full); };
   // copy j of the wave's CP of stage s
-  auto issue_one = [&](int s, int j) {
+  auto issue_one = [&](int s, int j, auto once) {
     const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);
     const int k0 = stage_of(s) * 128;  // past K: any bytes of the row, multiplied by zeros
     if (j < Sh::CPX) {
@@ -292,12 +333,10 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
       copy_rows(xsrc[j] + min(k0 + 16 * chunk_of(i, lane), A.K - 16), at + i * 1024);
     } else {
       const int i = Sh::CPW * wave + j - Sh::CPX;
-      copy_frag(wbase, wsrc[j - Sh::CPX] + (uint32_t)min(k0 + 16 * chunk_of(i, lane), A.K - 16), at + Sh::XB + i * 1024);
+      const uint32_t from = wsrc[j - Sh::CPX] + (uint32_t)min(k0 + 16 * chunk_of(i, lane), A.K - 16);
+      if constexpr (decltype(once)::value) copy_once(wbase, from, at + Sh::XB + i * 1024);
+      else copy_frag(wbase, from, at + Sh::XB + i * 1024);
     }
-  };
-  auto issue = [&](int s) {
-#pragma unroll
-    for (int j = 0; j < Sh::CP; ++j) issue_one(s, j);
   };
 
   i32x16_t acc[CB][TB];
@@ -318,7 +357,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
   // slot and the next stage's first reads are under way.  LIVE: the wave's row
   // blocks that hold rows (an expert's last tile); the others are not read or
   // multiplied, and a wave without any only copies.
-  auto reduce = [&](auto live) {
+  auto reduce = [&](auto live, auto once) {
     constexpr int LIVE = decltype(live)::value;
     // operand j of quarter ks of stage s: the channel blocks, then the row blocks
     auto load_one = [&](Frag& f, int s, int ks, int j) {
@@ -341,7 +380,7 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
         if (j < PRODUCTS)
           acc[j % CB][j / CB] =
               __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[j % CB], f.x[j / CB], acc[j % CB][j / CB], 0, 0, 0);
-        if (j < COPIES) issue_one(cs, j);
+        if (j < COPIES) issue_one(cs, j, once);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -379,18 +418,24 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
             __builtin_amdgcn_mfma_i32_32x32x32_i8(f0.w[j % CB], f0.x[j / CB], acc[j % CB][j / CB], 0, 0, 0);
     }
   };
+  auto run = [&](auto once) {
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (s <= last) issue(s);
-  if (S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 1)));
-  else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-  ring_barrier();
-  const int live = min(TB, (rows - wt * TB * 32 + 31) >> 5);
-  if (live == TB) reduce(std::integral_constant<int, TB>{});
-  else if (live <= 0) reduce(std::integral_constant<int, 0>{});
-  else if (TB == 4 && live == 3) reduce(std::integral_constant<int, TB == 4 ? 3 : 1>{});
-  else if (TB == 4 && live == 2) reduce(std::integral_constant<int, TB == 4 ? 2 : 1>{});
-  else reduce(std::integral_constant<int, 1>{});
+    for (int s = 0; s < S; ++s)
+      if (s <= last)
+#pragma unroll
+        for (int j = 0; j < Sh::CP; ++j) issue_one(s, j, once);
+    if (S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 1)));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    ring_barrier();
+    const int live = min(TB, (rows - wt * TB * 32 + 31) >> 5);
+    if (live == TB) reduce(std::integral_constant<int, TB>{}, once);
+    else if (live <= 0) reduce(std::integral_constant<int, 0>{}, once);
+    else if (TB == 4 && live == 3) reduce(std::integral_constant<int, TB == 4 ? 3 : 1>{}, once);
+    else if (TB == 4 && live == 2) reduce(std::integral_constant<int, TB == 4 ? 2 : 1>{}, once);
+    else reduce(std::integral_constant<int, 1>{}, once);
+  };
+  if (NT && it.blocks == 1) run(std::integral_constant<bool, NT>{});
+  else run(std::false_type{});
   __syncthreads();  // the ring is free
 
   // Epilogue: element v of acc[c][i] in lane l is channel acc_channel(l, v) of
@@ -448,13 +493,16 @@ __global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 
 }
 
 template <int TB, int CB, int WT, int WC, int S>
-hipError_t launch_tile(const I8Args& a, bool y_bf16, int cg, int rot, hipStream_t s) {
+hipError_t launch_tile(const I8Args& a, bool y_bf16, int cg, bool single, bool large, hipStream_t s) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   const long long blocks = row_blocks(a, Sh::BM) * ((a.N + Sh::BN - 1) / Sh::BN);
   if ((blocks + 8) * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
   const unsigned grid = (unsigned)((blocks + 7) / 8 * 8);
-  if (y_bf16) k_i8_tile<TB, CB, WT, WC, S, true><<<grid, WT * WC * 64, 0, s>>>(a, cg, rot);
-  else k_i8_tile<TB, CB, WT, WC, S, false><<<grid, WT * WC * 64, 0, s>>>(a, cg, rot);
+  auto go = [&](auto yb, auto nt) {
+    constexpr bool YB = decltype(yb)::value, NT = decltype(nt)::value;
+    k_i8_tile<TB, CB, WT, WC, S, YB, NT><<<grid, WT * WC * 64, 0, s>>>(a, cg, single);
+  };
+  dispatch(go, y_bf16, single && large);
   return hipGetLastError();
 }
 
@@ -472,28 +520,41 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
   auto items = [&](int BM, int BN) { return experts * ((avg + BM - 1) / BM) * ((a.N + BN - 1) / BN); };
   auto enough = [&](long long n, long long finer) { return 4 * n >= 3 * cus || (2 * n >= cus && finer > cus); };
   const long long n256 = items(256, 256), n128 = items(128, 256), n128s = items(128, 128);
+  // Weights that their experts' only row block reads, too large for the 256 MB
+  // last-level cache to hold until the next call, are read as not to be kept:
+  // 16 rows each of 8 experts, 470 MB: 84 -> 72 us; 16 x 28672 x 8192: 41 -> 37 us;
+  // 184 MB between other calls 37 -> 32 us (alone and warm 28.6 -> 31 us); 58 MB,
+  // warm: 10.9 -> 12.5 us.  Rows that share lines are fetched twice then (K =
+  // 1776, warm: 51 -> 62 us).
+  const bool large = a.K % 128 == 0 && reinterpret_cast<uintptr_t>(a.w) % 128 == 0 &&
+                     (long long)a.E * a.N * a.K >= 128 << 20;
   const int cg = 4;  // column blocks that share their rows in an XCD's L2 (2 and 8: within 2 %; 1: 10 % slower)
-  // 16384 rows of 8 experts, 4096 x 14336: 0.91, 128 x 256 1.05 ms; 128 rows each: 120 and 126 us;
+  // 16384 rows of 8 experts, 4096 x 14336: 0.91, 128 x 256 1.05 ms; 128 rows each: 113 and 124 us;
   // 5565 x 2832 x 1680 (154 items, 308 of 128 x 256): 39 and 53 us
-  if (avg > 112 && enough(n256, n128)) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, avg <= 192, s);
-  // 64 rows each of 8 experts: 93, 64 x 128 106 us; 2048 x 4096 x 4096 (128 items of 256 x 256): 37 and 43 us
-  if (avg > 48 && enough(n128, n128s)) return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, avg <= 128, s);
+  if (avg > 112 && enough(n256, n128)) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, avg <= 192, large, s);
+  // 64 rows each of 8 experts: 89, 64 x 128 106 us; 2048 x 4096 x 4096 (128 items of 256 x 256): 37 and 43 us
+  if (avg > 48 && enough(n128, n128s)) return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, avg <= 128, large, s);
   // 1003 x 6400 x 4096: 33 us, 128 x 256 40 us, 64 x 128 38 us
-  if (avg > 64 && 4 * n128s >= 3 * cus) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, s);
+  if (avg > 64 && 4 * n128s >= 3 * cus) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, large, s);
   // 512 x 4096 x 4096: 16.1 us, 128 x 128 17.3 us
-  if (avg > 32 && 4 * items(64, 128) >= 3 * cus) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, s);
-  // Few rows, two workgroups a CU, where the rounds are at least three
-  // quarters full: 16 rows each of 8 experts, 4096 x 14336 (448 items) 82 us,
-  // 64 x 64 88 us; 7 rows each of 64 experts, 1776 x 2464 (640): 75 and 62 us;
-  // 16 x 4096 x 14336 (56): 24 and 11 us
-  const long long n32 = items(32, 256), round = 2 * cus;
-  if (avg <= 32 && 3 * ((n32 + round - 1) / round * round) <= 4 * n32) return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, 1, s);
-  // 64 x 4096 x 14336: 12 us, 32 rows on private rings 22 us
-  if ((avg > 16 || a.E > 1) && 4 * items(64, 64) >= 3 * cus) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, 0, s);
+  if (avg > 32 && 4 * items(64, 128) >= 3 * cus) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, large, s);
+  // Few rows, two workgroups a CU: where three quarters of the CUs have one
+  // item, or the rounds of two are three quarters full: 16 x 4096 x 65536 (256
+  // items) 41 us, 64 x 64 47 us; 16 rows each of 8 experts, 4096 x 14336 (448)
+  // 72 and 78 us; 7 rows each of 64 experts, 1776 x 2464 (640): 75 and 62 us;
+  // 16 x 4096 x 40960 (160): 36 and 32 us
+  const long long n32 = items(32, 256), round = n32 <= cus ? cus : 2 * cus;
+  if (avg <= 32 && 3 * ((n32 + round - 1) / round * round) <= 4 * n32)
+    return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, true, large, s);
+  // 64 x 4096 x 14336: 12 us, 64 rows on private rings 16 us; 16 x 16384 x 16384: 40, 16 rows on them 45 us
+  if (4 * items(64, 64) >= 3 * cus) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, avg <= 64, large, s);
   // 16 x 14336 x 4096 (64 items of 64 channels): 11.4 us, 64 x 64 29 us
-  if (avg <= 16) return launch_rows<1, 2, 4, 2>(a, y_bf16, s);
-  // 64 x 14336 x 4096: 13.7 us, 64 x 64 29.5 us
-  return launch_rows<2, 2, 8, 1>(a, y_bf16, s);
+  if (avg <= 16) return launch_rows<1, 2, 4, 2>(a, y_bf16, large, s);
+  // 64 x 8192 x 8192 (256 items of 32 channels): 14.6 us, 32 rows 21 us; 64 x 14336 x 4096 (128): 18.4 and 13.6 us
+  if (avg > 32 && 4 * items(64, 32) >= 3 * cus) return launch_rows<4, 2, 4, 2>(a, y_bf16, large, s);
+  // 64 x 14336 x 4096: 13.6 us, 64 x 64 29.5 us; a ring of one stage for eight waves in place of two for four 13.8 us
+  // (64 x 8192 x 8192: 23 and 21 us)
+  return launch_rows<2, 2, 4, 2>(a, y_bf16, large, s);
 }
 
 }  // namespace moe

@@ -259,3 +259,55 @@ def test_quantize_codes():
         assert torch.equal(s, s2) and torch.equal((c.double() * s.double()[:, None]), v.double())
         _, codes_o, scales_o = oracle.quant_rows_i8(x.view(torch.int16).cpu().numpy().view(np.uint16))
         assert np.array_equal(c.cpu().numpy(), codes_o) and np.array_equal(s.cpu().numpy(), scales_o)
+
+
+# 128 MB of weights or more, which are read as not to be kept where an expert
+# has one row block: every tile shape, with experts of none, one and several
+# row blocks; the last two with weights off their 128-byte lines
+LARGE = {"t32x256": ([10, 0, 40, 3, 1, 9, 70, 8], 1024, 16392), "t64x64": ([30, 64, 0, 65, 1, 100, 17, 9], 8192, 2056),
+         "t64x128": ([40, 64, 65, 0, 30, 1, 100, 32], 2048, 8200), "t128x256": ([90, 128, 129, 0, 64, 20, 200, 33], 2048, 8200),
+         "t256x256": ([150, 256, 257, 0, 128, 100, 300, 33], 2048, 8200),
+         "t128x128": ([100, 128, 0, 129, 5, 160, 90, 64] * 2, 4096, 2056), "r16": ([11], 16384, 8200), "r32": ([30], 16384, 8200),
+         "r64": ([60], 16384, 8200), "r64_two_blocks": ([70], 16384, 8200),
+         "r16_two_blocks": ([20, 2], 16384, 4104), "short_lines": ([10, 0, 40, 3, 1, 9, 70, 8], 1040, 16392),
+         "shifted": ([10, 0, 40, 3, 1, 9, 70, 8], 1024, 16392)}
+
+
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name", LARGE)
+def test_large_weights(name, out):
+    counts, K, N = LARGE[name]
+    E, rows = len(counts), sum(counts)
+    log(f"matmul_i8 large weights {name} E={E} K={K} N={N} {out}")
+    w = codes((E * N * K + 128,), N)
+    at = 16 if name == "shifted" else 0
+    w = w[at:at + E * N * K].view(E, N, K)
+    assert E * N * K >= 1 << 27
+    offsets, perm, T, _ = grouped(counts, 2, E)
+    x, sx, sw = codes((T, K), K), scales((T,), 1), scales((E, N), 2)
+    if E == 1:
+        x, sx, offsets, perm = codes((rows, K), K), scales((rows,), 1), None, None
+    check(run(x, sx, w, sw, offsets, perm, 2, rows, out), exact(x, sx, w, sw, offsets, perm, 2, rows), out, "y")
+
+
+# private rings of 16, 32 and 64 rows, one and more row blocks, partial last stages
+PRIVATE = [(60, 272, 6168), (64, 2064, 6152), (100, 2064, 4104), (33, 4096, 7000), (130, 144, 2056), (20, 528, 4104),
+           (32, 16, 8200), (16, 2064, 4104)]
+
+
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,K,N", PRIVATE)
+def test_private_rings(R, K, N, out):
+    log(f"matmul_i8 private rings R={R} K={K} N={N} {out}")
+    x, w, sx, sw = codes((R, K), R + K), codes((1, N, K), N), scales((R,), 1), scales((1, N), 2)
+    check(run(x, sx, w, sw, None, None, 1, R, out), exact(x, sx, w, sw, None, None, 1, R), out, "y")
+
+
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("counts,K,N", [([60, 0, 33, 70], 272, 2056), ([40, 100, 1, 20], 2064, 2056), ([33, 40], 2048, 4104)])
+def test_private_rings_of_experts(counts, K, N, out):
+    log(f"matmul_i8 private rings {counts} K={K} N={N} {out}")
+    E = len(counts)
+    offsets, perm, T, rows = grouped(counts, 2, E)
+    x, w, sx, sw = codes((T, K), K), codes((E, N, K), N), scales((T,), 1), scales((E, N), 2)
+    check(run(x, sx, w, sw, offsets, perm, 2, rows, out), exact(x, sx, w, sw, offsets, perm, 2, rows), out, "y")
