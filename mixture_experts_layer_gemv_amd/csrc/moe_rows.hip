@@ -6,9 +6,11 @@
 // element, so bytes bound them; sums and statistics are fp32, and a value is
 // rounded once, when it is stored.  Measured at 8192 rows of 4096 bf16, in
 // parentheses the algorithmic bytes over the time (a large copy reaches 5.0
-// TB/s on this card): layer norm 27.6 us (4.9 TB/s), its gradients 42.5 us (4.7),
-// top-2 permute 39.4 us (5.1), its gradient and the combine 41.2 us (4.9), the
-// combine's gradient 66.3 us (5.1).
+// TB/s on this card): layer norm 24.5 us (5.5 TB/s), its gradients 41.4 us (4.9),
+// top-2 permute 38.4 us (5.2), its gradient and the combine 34.5 us (5.8), the
+// combine's gradient 66.0 us (5.1).
+#include <type_traits>
+
 #include "moe_kernels.hpp"
 #include "moe_rows.hpp"
 #include "moe_rows_index.hpp"
@@ -23,14 +25,23 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
+// 16 bytes; ONCE: of data that the caches need not keep.
+template <bool ONCE>
+__device__ __forceinline__ u32x4_t load16(const void* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(static_cast<const u32x4_t*>(p));
+  else return *static_cast<const u32x4_t*>(p);
+}
+
 // Eight consecutive elements starting at element i (a multiple of 8), as
-// loaded; converted only when they are used.
-template <bool BF16>
+// loaded; converted only when they are used.  (An fp32 load is of half lines,
+// which must stay cached until the other half is read: ONCE is for bf16.  Top-2
+// rows in fp32, 8192 x 4096, the combine's gradient: 119 us, 130 us with it.)
+template <bool BF16, bool ONCE>
 struct Raw8 {
   u32x4_t v[BF16 ? 1 : 2];
   __device__ __forceinline__ void load(const void* p, size_t i) {
     if constexpr (BF16) {
-      v[0] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + i);
+      v[0] = load16<ONCE>(static_cast<const uint16_t*>(p) + i);
     } else {
       const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(p) + i);
       v[0] = q[0];
@@ -55,9 +66,9 @@ struct Raw8 {
   }
 };
 
-template <bool BF16>
+template <bool BF16, bool ONCE>
 __device__ __forceinline__ void load8(const void* p, size_t i, float (&f)[8]) {
-  Raw8<BF16> r;
+  Raw8<BF16, ONCE> r;
   r.load(p, i);
   r.get(f);
 }
@@ -112,13 +123,13 @@ __device__ __forceinline__ float group_sum(float v, int n) {
 //
 // A team of NT threads (8, 16, 32 or a multiple of 64) owns a row; a block
 // holds one or more teams.  A thread keeps V times eight elements (norm_cols).
-template <bool BF16>
+template <bool BF16, bool ONCE>
 __device__ __forceinline__ void load_raw(u32x4_t (&v)[BF16 ? 1 : 2], const void* p, size_t row, NormCols c, int m) {
 #pragma unroll
   for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
     const int at = i ? c.hi : c.lo;
     v[i] = u32x4_t{0, 0, 0, 0};
-    if (at < m) v[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + (row + at) * (BF16 ? 2 : 4));
+    if (at < m) v[i] = load16<ONCE>(static_cast<const char*>(p) + (row + at) * (BF16 ? 2 : 4));
   }
 }
 
@@ -182,7 +193,7 @@ __device__ __forceinline__ float team_sum(float v, int NT, int first, float* slo
 // y = (x - mu) r gamma + beta, mu the row's mean (0 for the RMS norm), r = 1 /
 // sqrt(mean((x - mu)^2) + eps).  gamma and beta stay in registers from row to
 // row; the next row is loaded while this one is summed.
-template <bool BF16, int V, bool LAYER>
+template <bool BF16, int V, bool LAYER, bool ONCE>
 __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
   __shared__ float red[2][16];
   const int team = threadIdx.x / NT, teams = blockDim.x / NT, tid = threadIdx.x - team * NT;
@@ -203,7 +214,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
   auto fetch = [&](long long t) {
     if (t >= A.T) t = A.T - 1;  // read, never written
 #pragma unroll
-    for (int v = 0; v < V; ++v) load_raw<BF16>(next[v], A.x, (size_t)t * m, norm_cols(BF16, tid, NT, v), m);
+    for (int v = 0; v < V; ++v) load_raw<BF16, ONCE>(next[v], A.x, (size_t)t * m, norm_cols(BF16, tid, NT, v), m);
   };
   const long long stride = (long long)gridDim.x * teams;
   fetch((long long)blockIdx.x * teams + team);
@@ -257,7 +268,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
 // A thread adds its columns' dy h and dy over the rows its team takes.  The
 // block's sums are added in LDS and written as one row of partial sums, and
 // k_norm_wgrad adds those in block order: nothing depends on timing.
-template <bool BF16, int V, bool LAYER>
+template <bool BF16, int V, bool LAYER, bool ONCE>
 __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
   __shared__ float red[4][16];
   extern __shared__ float acc[];  // [2][m] where the block's sums are added
@@ -279,8 +290,8 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const NormCols c = norm_cols(BF16, tid, NT, v);
-      load_raw<BF16>(nx[v], A.x, (size_t)row * m, c, m);
-      load_raw<BF16>(ny[v], A.dy, (size_t)row * m, c, m);
+      load_raw<BF16, ONCE>(nx[v], A.x, (size_t)row * m, c, m);
+      load_raw<BF16, ONCE>(ny[v], A.dy, (size_t)row * m, c, m);
     }
     nmu = LAYER ? A.mean[row] : 0.0f;
     nr = A.rstd[row];
@@ -441,6 +452,7 @@ __device__ __forceinline__ int token_rows(const RowsArgs& A, int t, int lane) {
 }
 
 // out[inv[t*k+j]] = tok[t]: 16-byte chunks, whatever the type.
+template <bool ONCE>
 __global__ __launch_bounds__(256) void k_permute_rows(const RowsArgs A, int chunks, int slices) {
   const int lane = threadIdx.x & 63;
   const long long items = (long long)A.T * slices;
@@ -451,7 +463,7 @@ __global__ __launch_bounds__(256) void k_permute_rows(const RowsArgs A, int chun
     u32x4_t v[kSlice];
 #pragma unroll
     for (int i = 0; i < kSlice; ++i)
-      if (c0 + 64 * i < chunks) v[i] = src[c0 + 64 * i];
+      if (c0 + 64 * i < chunks) v[i] = load16<ONCE>(src + c0 + 64 * i);
     for (int j = 0; j < A.k; ++j) {
       const int r = __builtin_amdgcn_readlane(mine, j);
       if (r < 0) continue;
@@ -464,7 +476,7 @@ __global__ __launch_bounds__(256) void k_permute_rows(const RowsArgs A, int chun
 }
 
 // out[t] = sum_j w[t,j] rows[inv[t*k+j]], in order of j.
-template <bool RB, bool OB>
+template <bool RB, bool OB, bool ONCE>
 __global__ __launch_bounds__(256) void k_combine_rows(const RowsArgs A, int slices) {
   constexpr int V = 2;
   const int lane = threadIdx.x & 63, mv = A.m / 8;
@@ -486,7 +498,7 @@ __global__ __launch_bounds__(256) void k_combine_rows(const RowsArgs A, int slic
       for (int v = 0; v < V; ++v)
         if (c0 + 64 * v < mv) {
           float f[8];
-          load8<RB>(A.rows, (size_t)r * A.m + (size_t)(c0 + 64 * v) * 8, f);
+          load8<RB, ONCE>(A.rows, (size_t)r * A.m + (size_t)(c0 + 64 * v) * 8, f);
 #pragma unroll
           for (int q = 0; q < 8; ++q) s[v][q] = fmaf(wj, f[q], s[v][q]);
         }
@@ -499,7 +511,7 @@ __global__ __launch_bounds__(256) void k_combine_rows(const RowsArgs A, int slic
 
 // The combine's gradient, one block of up to four waves per token:
 // out[inv[t*k+j]] = w[t,j] dy[t], dw[t,j] = <dy[t], rows[inv[t*k+j]]>.
-template <bool TB, bool RB>
+template <bool TB, bool RB, bool ONCE>
 __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
   constexpr int V = 2;
   __shared__ float dots[4][64];
@@ -517,7 +529,7 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
         const int c = c0 + v * NT;
 #pragma unroll
         for (int q = 0; q < 8; ++q) d[v][q] = 0.0f;
-        if (c < mv) load8<TB>(A.tok, (size_t)t * A.m + (size_t)c * 8, d[v]);
+        if (c < mv) load8<TB, ONCE>(A.tok, (size_t)t * A.m + (size_t)c * 8, d[v]);
       }
       for (int j = 0; j < A.k; ++j) {
         const int r = __builtin_amdgcn_readlane(mine, j);
@@ -531,7 +543,7 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
             const size_t at = (size_t)r * A.m + (size_t)c * 8;
             if (A.dw) {
               float f[8];
-              load8<RB>(A.rows, at, f);
+              load8<RB, ONCE>(A.rows, at, f);
 #pragma unroll
               for (int q = 0; q < 8; ++q) dot = fmaf(d[v][q], f[q], dot);
             }
@@ -568,15 +580,30 @@ unsigned wave_grid(long long items) {  // four waves a block, an item each
   return blocks < kMaxGrid ? (unsigned)blocks : (unsigned)kMaxGrid;
 }
 
-}  // namespace
+// f(flags ...) with each flag known to the compiler.
+template <class F>
+void dispatch(F f) {
+  f();
+}
+template <class F, class... Flags>
+void dispatch(F f, bool flag, Flags... rest) {
+  if (flag) dispatch([&](auto... r) { f(std::true_type{}, r...); }, rest...);
+  else dispatch([&](auto... r) { f(std::false_type{}, r...); }, rest...);
+}
 
-#define MOE_NORM(KERNEL, ...)                               \
-  do {                                                      \
-    if (bf16 && layer) KERNEL(true, true)<<<__VA_ARGS__;     \
-    else if (bf16) KERNEL(true, false)<<<__VA_ARGS__;        \
-    else if (layer) KERNEL(false, true)<<<__VA_ARGS__;       \
-    else KERNEL(false, false)<<<__VA_ARGS__;                 \
-  } while (0)
+// A call that moves half of the 256 MB last-level cache or more reads its
+// inputs as data not to be kept (ONCE), which leaves the cache to what it writes
+// for the next operator.  8192 x 4096 bf16: layer norm 27.3 -> 24.6 us, its
+// gradients 43.2 -> 41.4, top-2 permute 39.9 -> 38.7, combine 41.1 -> 34.7; norm,
+// permute and combine in turn 95 -> 84 us, their gradients 140 -> 128.  Below it
+// the inputs may still be cached (16384 x 1024, norm, called again on the same
+// rows: 12.8 -> 14.5 us).  Outputs written past the caches would take 22.6, 42.6,
+// 30.2 and 37.7 us, and their next reader would pay for it (the three in turn:
+// 100 us).
+bool large(long long bytes) { return bytes >= 128 << 20; }
+long long bytes_of(long long rows, int m, bool bf16) { return rows * m * (bf16 ? 2 : 4); }
+
+}  // namespace
 
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
@@ -584,12 +611,13 @@ hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus
   const int V = norm_vecs(a.m), nt = norm_threads(a.m), teams = norm_fwd_teams(nt), threads = nt * teams;
   const long long blocks = ((long long)a.T + teams - 1) / teams, most = (long long)cus * (V == 1 ? 2048 / threads : 1);
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-#define MOE_FWD1(B, L) k_norm_fwd<B, 1, L>
-#define MOE_FWD2(B, L) k_norm_fwd<B, 2, L>
-  if (V == 1) MOE_NORM(MOE_FWD1, grid, threads, 0, s>>>(a, nt));
-  else MOE_NORM(MOE_FWD2, grid, threads, 0, s>>>(a, nt));
-#undef MOE_FWD1
-#undef MOE_FWD2
+  dispatch(
+      [&](auto b, auto l, auto big) {
+        constexpr bool B = decltype(b)::value, L = decltype(l)::value, ONCE = decltype(big)::value;
+        if (V == 1) k_norm_fwd<B, 1, L, ONCE><<<grid, threads, 0, s>>>(a, nt);
+        else k_norm_fwd<B, 2, L, ONCE><<<grid, threads, 0, s>>>(a, nt);
+      },
+      bf16, layer, large(2 * bytes_of(a.T, a.m, bf16)));
   return hipGetLastError();
 }
 
@@ -599,25 +627,27 @@ hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cu
   const int V = norm_vecs(a.m), nt = norm_threads(a.m), threads = nt * norm_bwd_teams(nt);
   const unsigned grid = (unsigned)norm_bwd_blocks(a.T, a.m, cus);
   const size_t lds = threads > (nt < 64 ? 64 : nt) ? 2 * sizeof(float) * (size_t)a.m : 0;  // at most 2048 columns
-#define MOE_BWD1(B, L) k_norm_bwd<B, 1, L>
-#define MOE_BWD2(B, L) k_norm_bwd<B, 2, L>
-  if (V == 1) MOE_NORM(MOE_BWD1, grid, threads, lds, s>>>(a, nt));
-  else MOE_NORM(MOE_BWD2, grid, threads, lds, s>>>(a, nt));
-#undef MOE_BWD1
-#undef MOE_BWD2
+  dispatch(
+      [&](auto b, auto l, auto big) {
+        constexpr bool B = decltype(b)::value, L = decltype(l)::value, ONCE = decltype(big)::value;
+        if (V == 1) k_norm_bwd<B, 1, L, ONCE><<<grid, threads, lds, s>>>(a, nt);
+        else k_norm_bwd<B, 2, L, ONCE><<<grid, threads, lds, s>>>(a, nt);
+      },
+      bf16, layer, large((a.out ? 3 : 2) * bytes_of(a.T, a.m, bf16)));
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !a.partial || grid == 1) return e;
   k_norm_wgrad<<<dim3((unsigned)((a.m + 31) / 32), layer ? 2 : 1), 512, 0, s>>>(a.partial, (int)grid, a.m, a.dgamma,
                                                                                layer ? a.dbeta : nullptr);
   return hipGetLastError();
 }
-#undef MOE_NORM
 
 hipError_t launch_permute_rows(const RowsArgs& a, bool bf16, hipStream_t s) {
   if (a.T <= 0 || a.R <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.k < 1 || a.k > 64) return hipErrorInvalidValue;
   const int chunks = bf16 ? a.m / 8 : a.m / 4;
   const int slices = (chunks + 64 * kSlice - 1) / (64 * kSlice);
-  k_permute_rows<<<wave_grid((long long)a.T * slices), 256, 0, s>>>(a, chunks, slices);
+  const unsigned g = wave_grid((long long)a.T * slices);
+  dispatch([&](auto big) { k_permute_rows<decltype(big)::value><<<g, 256, 0, s>>>(a, chunks, slices); },
+           large(bytes_of((long long)a.T + a.R, a.m, bf16)));
   return hipGetLastError();
 }
 
@@ -626,10 +656,11 @@ hipError_t launch_combine_rows(const RowsArgs& a, bool rows_bf16, bool out_bf16,
   if (a.m <= 0 || a.m % 8 || a.k < 1 || a.k > 64) return hipErrorInvalidValue;
   const int slices = (a.m / 8 + 127) / 128;
   const unsigned g = wave_grid((long long)a.T * slices);
-  if (rows_bf16 && out_bf16) k_combine_rows<true, true><<<g, 256, 0, s>>>(a, slices);
-  else if (rows_bf16) k_combine_rows<true, false><<<g, 256, 0, s>>>(a, slices);
-  else if (out_bf16) k_combine_rows<false, true><<<g, 256, 0, s>>>(a, slices);
-  else k_combine_rows<false, false><<<g, 256, 0, s>>>(a, slices);
+  dispatch(
+      [&](auto rb, auto ob, auto big) {
+        k_combine_rows<decltype(rb)::value, decltype(ob)::value, decltype(big)::value><<<g, 256, 0, s>>>(a, slices);
+      },
+      rows_bf16, out_bf16, large(bytes_of(a.R, a.m, rows_bf16) + bytes_of(a.T, a.m, out_bf16)));
   return hipGetLastError();
 }
 
@@ -639,10 +670,12 @@ hipError_t launch_combine_rows_backward(const RowsArgs& a, bool tok_bf16, bool r
   int waves = (a.m / 8 + 127) / 128;
   if (waves > 4) waves = 4;
   const unsigned g = a.T < kMaxGrid ? (unsigned)a.T : (unsigned)kMaxGrid;
-  if (tok_bf16 && rows_bf16) k_combine_rows_bwd<true, true><<<g, waves * 64, 0, s>>>(a);
-  else if (tok_bf16) k_combine_rows_bwd<true, false><<<g, waves * 64, 0, s>>>(a);
-  else if (rows_bf16) k_combine_rows_bwd<false, true><<<g, waves * 64, 0, s>>>(a);
-  else k_combine_rows_bwd<false, false><<<g, waves * 64, 0, s>>>(a);
+  const int passes = (a.dw ? 1 : 0) + (a.out ? 1 : 0);
+  dispatch(
+      [&](auto tb, auto rb, auto big) {
+        k_combine_rows_bwd<decltype(tb)::value, decltype(rb)::value, decltype(big)::value><<<g, waves * 64, 0, s>>>(a);
+      },
+      tok_bf16, rows_bf16, large(bytes_of(a.T, a.m, tok_bf16) + passes * bytes_of(a.R, a.m, rows_bf16)));
   return hipGetLastError();
 }
 

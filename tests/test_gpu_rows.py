@@ -463,3 +463,65 @@ def test_as_many_tokens_as_an_int_counts():
     assert float(x.amax()) == 0.0 and float(x.amin()) == 0.0
     del x, inv, w
     torch.cuda.empty_cache()
+
+
+# Calls that move 128 MB or more read their inputs as data not to be kept; the
+# same rows in smaller calls must give the same bits, row by row.
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("layer", [True, False], ids=["layer", "rms"])
+@pytest.mark.parametrize("m", [1000, 4096, 16376])
+def test_large_norms_match_small_ones(m, layer, dtype):
+    es = 2 if dtype == BF16 else 4
+    T = 4 * ((64 << 20) // (4 * m * es) + 1)
+    kind = M.MOE_NORM_LAYER if layer else M.MOE_NORM_RMS
+    x, dy, gamma = rnd((T, m), dtype, 1, shift=0.25), rnd((T, m), dtype, 2), rnd((m,), F32, 3)
+    beta = rnd((m,), F32, 4) if layer else None
+
+    def call(lo, n):
+        xs, dys = x[lo:lo + n], dy[lo:lo + n]
+        y, dx = torch.empty_like(xs), torch.empty_like(xs)
+        mean, rstd = torch.empty(n, device="cuda") if layer else None, torch.empty(n, device="cuda")
+        dg, db = torch.empty(m, device="cuda"), torch.empty(m, device="cuda") if layer else None
+        M.moe_norm_forward(xs, CODE[dtype], kind, gamma, beta, 1e-5, n, m, y, mean, rstd)
+        b = M.moe_norm_backward_workspace_size(n, m)
+        ws = torch.empty(max(b, 256), dtype=torch.uint8, device="cuda")
+        M.moe_norm_backward(dys, xs, CODE[dtype], kind, gamma, mean, rstd, n, m, dx, dg, db, ws, b)
+        return y, dx, rstd, dg, db
+
+    y, dx, rstd, dg, db = call(0, T)
+    n = T // 4
+    parts = [call(i * n, n) for i in range(4)]
+    for whole, at in [(y, 0), (dx, 1), (rstd, 2)]:
+        assert torch.equal(whole, torch.cat([p[at] for p in parts]))
+    for whole, at in [(dg, 3), (db, 4)]:
+        if whole is not None:  # each sum is within T u of its terms' magnitudes: |dy h| <= |dy| |h|, |h| <= sqrt(m)
+            s = sum(p[at].double() for p in parts)
+            mag = dy.double().abs().sum(0) * (m**0.5 if at == 3 else 1.0)
+            assert bool(((whole.double() - s).abs() <= 2 * T * u * mag).all())
+
+
+@pytest.mark.parametrize("pair", PAIRS, ids=ids)
+def test_large_rows_match_small_ones(pair):
+    td, rd = pair  # of token rows and of expert rows
+    T, k, m = 8192, 2, 4104
+    R, n = T * k, T // 4
+    g = torch.Generator().manual_seed(5)
+    small = [torch.randperm(n * k, generator=g).to(torch.int32).cuda() for _ in range(4)]  # a quarter's tokens, its rows
+    inv = torch.cat([p + i * n * k for i, p in enumerate(small)])
+    x, yp, w = rnd((T, m), td, 1), rnd((R, m), rd, 2), rnd((T, k), F32, 3)
+
+    def call(t0, T, inv):
+        xs, ys, ws, R = x[t0:t0 + T], yp[t0 * k:(t0 + T) * k], w[t0:t0 + T], T * k
+        xp, out, back = torch.empty(R, m, dtype=td, device="cuda"), torch.empty_like(xs), torch.empty_like(xs)
+        dyp, dw = torch.empty_like(ys), torch.empty_like(ws)
+        M.moe_permute_rows(xs, CODE[td], inv, T, m, k, R, xp)
+        M.moe_permute_rows_backward(ys, CODE[rd], inv, T, m, k, R, back, CODE[td])
+        M.moe_combine_rows(ys, CODE[rd], inv, ws, T, m, k, R, out, CODE[td])
+        M.moe_combine_rows_backward(xs, CODE[td], ys, CODE[rd], inv, ws, T, m, k, R, dyp, dw)
+        return xp, back, out, dyp, dw
+
+    whole = call(0, T, inv)
+    parts = [call(i * n, n, small[i]) for i in range(4)]
+    for i, a in enumerate(whole):
+        assert torch.equal(a, torch.cat([p[i] for p in parts]))
+    assert torch.equal(whole[0][inv.long()], x.repeat_interleave(k, 0))
