@@ -21,6 +21,7 @@ namespace {
 // (HIP's own uint4 is a struct whose arrays the compiler does not keep in
 // registers once their loads are conditional)
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -32,45 +33,15 @@ __device__ __forceinline__ u32x4_t load16(const void* p) {
   else return *static_cast<const u32x4_t*>(p);
 }
 
-// Eight consecutive elements starting at element i (a multiple of 8), as
-// loaded; converted only when they are used.  (An fp32 load is of half lines,
-// which must stay cached until the other half is read: ONCE is for bf16.  Top-2
-// rows in fp32, 8192 x 4096, the combine's gradient: 119 us, 130 us with it.)
-template <bool BF16, bool ONCE>
-struct Raw8 {
-  u32x4_t v[BF16 ? 1 : 2];
-  __device__ __forceinline__ void load(const void* p, size_t i) {
-    if constexpr (BF16) {
-      v[0] = load16<ONCE>(static_cast<const uint16_t*>(p) + i);
-    } else {
-      const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(p) + i);
-      v[0] = q[0];
-      v[1] = q[1];
-    }
-  }
-  __device__ __forceinline__ void clear() {
-    v[0] = u32x4_t{0, 0, 0, 0};
-    if constexpr (!BF16) v[1] = u32x4_t{0, 0, 0, 0};
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (BF16) {
-        f[2 * j] = __uint_as_float(v[0][j] << 16);
-        f[2 * j + 1] = __uint_as_float(v[0][j] & 0xFFFF0000u);
-      } else {
-        f[j] = __uint_as_float(v[0][j]);
-        f[4 + j] = __uint_as_float(v[1][j]);
-      }
-    }
-  }
-};
-
-template <bool BF16, bool ONCE>
+// Eight consecutive bf16 starting at element i (a multiple of 8).
+template <bool ONCE>
 __device__ __forceinline__ void load8(const void* p, size_t i, float (&f)[8]) {
-  Raw8<BF16, ONCE> r;
-  r.load(p, i);
-  r.get(f);
+  const u32x4_t v = load16<ONCE>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float(v[j] << 16);
+    f[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
+  }
 }
 
 // Two fp32 -> two bf16, round to nearest even (the hardware conversion).
@@ -78,16 +49,9 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
-template <bool BF16>
 __device__ __forceinline__ void store8(void* p, size_t i, const float (&f)[8]) {
-  if constexpr (BF16) {
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i) =
-        u32x4_t{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7])};
-  } else {
-    f32x4_t* q = reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + i);
-    q[0] = f32x4_t{f[0], f[1], f[2], f[3]};
-    q[1] = f32x4_t{f[4], f[5], f[6], f[7]};
-  }
+  *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i) =
+      u32x4_t{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7])};
 }
 
 // v plus the value that the DPP control CTRL moves to each lane (0 where none does).
@@ -150,7 +114,7 @@ __device__ __forceinline__ void from_raw(const u32x4_t (&v)[BF16 ? 1 : 2], float
 template <bool BF16>
 __device__ __forceinline__ void store_row(void* p, size_t row, NormCols c, int m, const float (&f)[8]) {
   if constexpr (BF16) {
-    if (c.lo < m) store8<true>(p, row + c.lo, f);
+    if (c.lo < m) store8(p, row + c.lo, f);
   } else {
     if (c.lo < m) *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + c.lo) = f32x4_t{f[0], f[1], f[2], f[3]};
     if (c.hi < m) *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + c.hi) = f32x4_t{f[4], f[5], f[6], f[7]};
@@ -440,10 +404,10 @@ __global__ __launch_bounds__(512) void k_norm_wgrad(const float* __restrict__ pa
 
 // ---- rows in expert order ---------------------------------------------------------
 //
-// One wave per (token, 256-vector slice of its row).  An assignment's row is
+// One wave per (token, slice of its row).  An assignment's row is
 // inv[t*k + j]; a value outside [0, R) means that it has none (dropped): it
 // is not written, adds nothing and gets a zero weight gradient.
-constexpr int kSlice = 4;  // 8-element vectors per lane
+constexpr int kSlice = 4;  // 16-byte vectors per lane of a permuted slice
 
 // The k rows of token t, one per lane (k <= 64).
 __device__ __forceinline__ int token_rows(const RowsArgs& A, int t, int lane) {
@@ -475,14 +439,61 @@ __global__ __launch_bounds__(256) void k_permute_rows(const RowsArgs A, int chun
   }
 }
 
+// The eight elements of a row at columns c (slab_cols), 0 past m: lanes past it
+// load the row's end, so that the loads depend on no branch.  ONCE as in load16.
+template <bool BF16, bool FOURS, bool ONCE>
+__device__ __forceinline__ void load_cols(const void* p, size_t row, NormCols c, int m, float (&f)[8]) {
+  if constexpr (!FOURS) {
+    load8<ONCE>(p, row + min(c.lo, m - 8), f);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const size_t at = row + min(h ? c.hi : c.lo, m - 4);
+      if constexpr (BF16) {
+        const u32x2_t v = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f[4 * h + 2 * j] = __uint_as_float(v[j] << 16);
+          f[4 * h + 2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
+        }
+      } else {
+        const u32x4_t v = load16<ONCE>(static_cast<const float*>(p) + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[4 * h + j] = __uint_as_float(v[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = (j < 4 ? c.lo : c.hi) < m ? f[j] : 0.0f;
+}
+
+template <bool BF16, bool FOURS>
+__device__ __forceinline__ void store_cols(void* p, size_t row, NormCols c, int m, const float (&f)[8]) {
+  if constexpr (!FOURS) {
+    if (c.lo < m) store8(p, row + c.lo, f);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = h ? c.hi : c.lo;
+      if (at >= m) continue;
+      const float* g = f + 4 * h;
+      if constexpr (BF16)
+        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + row + at) = u32x2_t{pack2_bf16(g[0], g[1]), pack2_bf16(g[2], g[3])};
+      else
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + at) = f32x4_t{g[0], g[1], g[2], g[3]};
+    }
+  }
+}
+
 // out[t] = sum_j w[t,j] rows[inv[t*k+j]], in order of j.
 template <bool RB, bool OB, bool ONCE>
 __global__ __launch_bounds__(256) void k_combine_rows(const RowsArgs A, int slices) {
   constexpr int V = 2;
-  const int lane = threadIdx.x & 63, mv = A.m / 8;
+  constexpr bool FOURS = !RB || !OB;
+  const int lane = threadIdx.x & 63;
   const long long items = (long long)A.T * slices;
   for (long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += 4LL * gridDim.x) {
-    const int t = (int)(item / slices), c0 = (int)(item % slices) * 64 * V + lane;
+    const int t = (int)(item / slices), slab = (int)(item % slices) * V;
     const int mine = token_rows(A, t, lane);
     const float wl = lane < A.k ? (A.w ? A.w[(size_t)t * A.k + lane] : 1.0f) : 0.0f;
     float s[V][8];
@@ -495,17 +506,16 @@ __global__ __launch_bounds__(256) void k_combine_rows(const RowsArgs A, int slic
       if (r < 0) continue;
       const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), j));
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (c0 + 64 * v < mv) {
-          float f[8];
-          load8<RB, ONCE>(A.rows, (size_t)r * A.m + (size_t)(c0 + 64 * v) * 8, f);
+      for (int v = 0; v < V; ++v) {
+        float f[8];
+        load_cols<RB, FOURS, ONCE>(A.rows, (size_t)r * A.m, slab_cols(FOURS, lane, slab + v), A.m, f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) s[v][q] = fmaf(wj, f[q], s[v][q]);
-        }
+        for (int q = 0; q < 8; ++q) s[v][q] = fmaf(wj, f[q], s[v][q]);
+      }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (c0 + 64 * v < mv) store8<OB>(A.out, (size_t)t * A.m + (size_t)(c0 + 64 * v) * 8, s[v]);
+      store_cols<OB, FOURS>(A.out, (size_t)t * A.m, slab_cols(FOURS, lane, slab + v), A.m, s[v]);
   }
 }
 
@@ -514,23 +524,20 @@ __global__ __launch_bounds__(256) void k_combine_rows(const RowsArgs A, int slic
 template <bool TB, bool RB, bool ONCE>
 __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
   constexpr int V = 2;
+  constexpr bool FOURS = !TB || !RB;
   __shared__ float dots[4][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, NT = blockDim.x, waves = NT >> 6;
-  const int mv = A.m / 8;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int slabs = (A.m + 511) / 512;
   for (long long i = blockIdx.x; i < A.T; i += gridDim.x) {  // the step past the last token may pass 2^31
     const int t = (int)i;
     const int mine = token_rows(A, t, lane);
     const float wl = lane < A.k && A.w ? A.w[(size_t)t * A.k + lane] : 0.0f;
     dots[wave][lane] = 0.0f;
-    for (int c0 = tid; c0 < (mv + 63) / 64 * 64; c0 += NT * V) {
+    for (int slab = wave; slab < slabs; slab += waves * V) {
       float d[V][8];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = c0 + v * NT;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) d[v][q] = 0.0f;
-        if (c < mv) load8<TB, ONCE>(A.tok, (size_t)t * A.m + (size_t)c * 8, d[v]);
-      }
+      for (int v = 0; v < V; ++v)
+        load_cols<TB, FOURS, ONCE>(A.tok, (size_t)t * A.m, slab_cols(FOURS, lane, slab + v * waves), A.m, d[v]);
       for (int j = 0; j < A.k; ++j) {
         const int r = __builtin_amdgcn_readlane(mine, j);
         if (r < 0) continue;
@@ -538,21 +545,18 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const int c = c0 + v * NT;
-          if (c < mv) {
-            const size_t at = (size_t)r * A.m + (size_t)c * 8;
-            if (A.dw) {
-              float f[8];
-              load8<RB, ONCE>(A.rows, at, f);
+          const NormCols c = slab_cols(FOURS, lane, slab + v * waves);
+          if (A.dw) {
+            float f[8];
+            load_cols<RB, FOURS, ONCE>(A.rows, (size_t)r * A.m, c, A.m, f);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) dot = fmaf(d[v][q], f[q], dot);
-            }
-            if (A.out) {
-              float o[8];
+            for (int q = 0; q < 8; ++q) dot = fmaf(d[v][q], f[q], dot);
+          }
+          if (A.out) {
+            float o[8];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] = wj * d[v][q];
-              store8<RB>(A.out, at, o);
-            }
+            for (int q = 0; q < 8; ++q) o[q] = wj * d[v][q];
+            store_cols<RB, FOURS>(A.out, (size_t)r * A.m, c, A.m, o);
           }
         }
         if (A.dw) {

@@ -22,6 +22,14 @@ MOE_HD inline NormCols norm_cols(bool bf16, int tid, int NT, int v) {
   return {4 * (tid + 2 * v * NT), 4 * (tid + (2 * v + 1) * NT)};
 }
 
+// The same for a lane of a wave that takes 512 columns of a row: eights where
+// all of the data is bf16, else twice four (fp32 rows, 8192 x 4096, top-2: the
+// combine 64 -> 56 us, its gradient 118 -> 115).
+MOE_HD inline NormCols slab_cols(bool fours, int lane, int slab) {
+  const int at = 512 * slab;
+  return fours ? NormCols{at + 4 * lane, at + 256 + 4 * lane} : NormCols{at + 8 * lane, at + 8 * lane + 4};
+}
+
 // Vectors of 8 per thread, and threads of a team, for rows of m.
 MOE_HD inline int norm_vecs(int m) { return m <= 8192 ? 1 : 2; }
 MOE_HD inline int norm_threads(int m) {

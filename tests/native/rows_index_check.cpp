@@ -140,6 +140,22 @@ static void norm() {
       for (int i = 0; i < m; ++i) CHECK(col[i] == 1, "m %d column %d: %d times", m, i, col[i]);
     }
   }
+  for (int m = 8; m <= 4200; m += 8)  // a row by slabs, and the loads of lanes past its end
+    for (int fours = 0; fours < 2; ++fours) {
+      std::vector<char> col(m, 0);
+      for (int slab = 0; slab < (m + 511) / 512; ++slab)
+        for (int lane = 0; lane < 64; ++lane) {
+          const moe::NormCols c = moe::slab_cols(fours, lane, slab);
+          CHECK(c.lo >= 512 * slab && c.hi + 4 <= 512 * (slab + 1), "slab %d lane %d", slab, lane);
+          CHECK(fours || (c.lo % 8 == 0 && c.hi == c.lo + 4 && (c.lo < m) == (c.hi < m)), "slab %d lane %d", slab, lane);
+          for (int f : {c.lo, c.hi})
+            if (f < m) {
+              CHECK(f % 4 == 0 && f + 4 <= m, "m %d column %d", m, f);
+              for (int j = 0; j < 4; ++j) col.at(f + j)++;
+            }
+        }
+      for (int i = 0; i < m; ++i) CHECK(col[i] == 1, "m %d column %d: %d times", m, i, col[i]);
+    }
   for (int cus : {1, 104, 256, 304})
     for (int m : {8, 64, 256, 512, 1000, 2048, 4096, 8192, 8200, 16384})
       for (int T : {0, 1, 2, 4, 5, 63, 64, 65, 255, 256, 257, 777, 1000, 4097, 100000, 2147483647}) {
