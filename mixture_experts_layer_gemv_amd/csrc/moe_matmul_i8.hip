@@ -289,8 +289,9 @@ hipError_t launch_rows(const I8Args& a, bool y_bf16, bool large, hipStream_t s) 
 // (32 x 256 tiles) stream their weights at 6.5 TB/s.  NT: an expert's weights
 // that only one row block reads are not kept.
 template <int TB, int CB, int WT, int WC, int S, bool YB, bool NT>
-__global__ __launch_bounds__(WT* WC * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_i8_tile(const I8Args A, int cg,
-                                                                                                     bool rotate) {
+__global__ __launch_bounds__(WT* WC * 64)
+    __attribute__((amdgpu_waves_per_eu(TileShape<TB, CB, WT, WC, S>::per_simd, TileShape<TB, CB, WT, WC, S>::per_simd)))
+void k_i8_tile(const I8Args A, int cg, bool rotate) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   __shared__ __attribute__((aligned(1024))) unsigned char ring[S][Sh::XB + Sh::WB];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -538,12 +539,14 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
   if (avg > 64 && 4 * n128s >= 3 * cus) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, large, s);
   // 512 x 4096 x 4096: 16.1 us, 128 x 128 17.3 us
   if (avg > 32 && 4 * items(64, 128) >= 3 * cus) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, large, s);
-  // Few rows, two workgroups a CU: where three quarters of the CUs have one
-  // item, or the rounds of two are three quarters full: 16 x 4096 x 65536 (256
-  // items) 41 us, 64 x 64 47 us; 16 rows each of 8 experts, 4096 x 14336 (448)
-  // 72 and 78 us; 7 rows each of 64 experts, 1776 x 2464 (640): 75 and 62 us;
-  // 16 x 4096 x 40960 (160): 36 and 32 us
-  const long long n32 = items(32, 256), round = n32 <= cus ? cus : 2 * cus;
+  // Few rows: one workgroup a CU with a ring of three stages where a round of
+  // them is five eighths full (16 x 4096 x 49152, 192 items: 31.6, 64 x 64 39.6
+  // us; 16 x 4096 x 32768, 128 items: 27.0 and 25.4), else two with two stages
+  // where the rounds are three quarters full (16 rows each of 8 experts, 4096 x
+  // 14336, 448 items: 72 and 78 us; 7 rows each of 64 experts, 1776 x 2464, 640
+  // items: 75 and 62 us).
+  const long long n32 = items(32, 256), round = 2 * cus;
+  if (avg <= 32 && n32 <= cus && 8 * n32 >= 5 * cus) return launch_tile<1, 2, 1, 4, 3>(a, y_bf16, cg, true, large, s);
   if (avg <= 32 && 3 * ((n32 + round - 1) / round * round) <= 4 * n32)
     return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, true, large, s);
   // 64 x 4096 x 14336: 12 us, 64 rows on private rings 16 us; 16 x 16384 x 16384: 40, 16 rows on them 45 us

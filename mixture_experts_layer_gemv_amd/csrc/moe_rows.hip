@@ -478,7 +478,8 @@ __device__ __forceinline__ void store_cols(void* p, size_t row, NormCols c, int 
       if (at >= m) continue;
       const float* g = f + 4 * h;
       if constexpr (BF16)
-        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + row + at) = u32x2_t{pack2_bf16(g[0], g[1]), pack2_bf16(g[2], g[3])};
+        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + row + at) =
+            u32x2_t{pack2_bf16(g[0], g[1]), pack2_bf16(g[2], g[3])};
       else
         *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + row + at) = f32x4_t{g[0], g[1], g[2], g[3]};
     }

@@ -86,6 +86,8 @@ struct TileShape {
   static constexpr int XB = BM * 128, WB = BN * 128;  // bytes of a stage
   static constexpr int CPX = BM / 8 / waves, CPW = BN / 8 / waves, CP = CPX + CPW;  // copies per wave and stage
   static constexpr int RING = S * (XB + WB);
+  // Waves a SIMD holds (of 4 a CU): one workgroup of eight waves, or as many of four as the LDS takes, up to two.
+  static constexpr int per_simd = waves > 4 || 2 * RING <= 160 * 1024 ? 2 : 1;
   static_assert(BM % (8 * waves) == 0 && BN % (8 * waves) == 0, "every wave issues the same copies");
   static_assert(CP * (S - 1) <= 63, "vmcnt holds at most 63");
   // Epilogue: a wave stages 32 rows of its 32 CB channels of ES bytes, padded

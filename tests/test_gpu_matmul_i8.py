@@ -311,3 +311,15 @@ def test_private_rings_of_experts(counts, K, N, out):
     offsets, perm, T, rows = grouped(counts, 2, E)
     x, w, sx, sw = codes((T, K), K), codes((E, N, K), N), scales((T,), 1), scales((E, N), 2)
     check(run(x, sx, w, sw, offsets, perm, 2, rows, out), exact(x, sx, w, sw, offsets, perm, 2, rows), out, "y")
+
+
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K", [16, 272, 384, 1040, 4096])
+@pytest.mark.parametrize("E,N", [(8, 5128), (1, 41000)])
+def test_few_rows_of_wide_tiles(E, N, K, out):
+    """One round of 32 x 256 tiles, with one to many stages and a partial last one."""
+    counts = [10, 0, 40, 3, 1, 9, 70, 8] if E == 8 else [17]
+    log(f"matmul_i8 wide tiles {counts} K={K} N={N} {out}")
+    offsets, perm, T, rows = grouped(counts, 2, E)
+    x, w, sx, sw = codes((T, K), K), codes((E, N, K), N), scales((T,), 1), scales((E, N), 2)
+    check(run(x, sx, w, sw, offsets, perm, 2, rows, out), exact(x, sx, w, sw, offsets, perm, 2, rows), out, "y")
