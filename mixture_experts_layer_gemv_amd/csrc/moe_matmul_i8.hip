@@ -176,7 +176,7 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   const int steps = (A.K + 127) / 128;
   const int lo = (int)((long long)steps * wave / W), hi = (int)((long long)steps * (wave + 1) / W);
   const int rot = lo < hi ? it.nb % (hi - lo) : 0;
-  auto stage_of = [&](int s) { return s + rot < hi ? s + rot : s + rot - (hi - lo); };
+  auto stage_of = [&](int s) { return turned(s, rot, lo, hi); };
   auto issue = [&](int s, int slot, auto once) {
     const int k0 = stage_of(min(s, hi - 1)) * 128;  // past K: any bytes of the row, multiplied by zeros
     const uint32_t at = at0 + (uint32_t)slot * STAGE;
@@ -324,7 +324,7 @@ void k_i8_tile(const I8Args A, int cg, bool rotate) {
   // (16 rows each of 8 experts, 470 MB of weights: 84 against 72 us).  A partial stage
   // stays the last.
   const int full = A.K / 128, rot = rotate && full ? it.nb % full : 0;
-  auto stage_of = [&](int s) { return s >= full ? s : (s + rot < full ? s + rot : s + rot - full); };
+  auto stage_of = [&](int s) { return s >= full ? s : turned(s, rot, 0, full); };
   // copy j of the wave's CP of stage s
   auto issue_one = [&](int s, int j, auto once) {
     const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);

@@ -77,6 +77,10 @@ MOE_HD inline int chunk_of(int i, int lane) { return (lane & 7) ^ ((4 * i + (lan
 MOE_HD inline int operand32(int lane, int ks) { return (lane & 31) * 128 + 16 * line_place(lane & 31, 2 * ks + (lane >> 5)); }
 MOE_HD inline int operand16(int lane, int ks) { return (lane & 15) * 128 + 16 * line_place(lane & 15, 4 * ks + (lane >> 4)); }
 
+// Stage s of [lo, hi) in a walk that begins rot stages (of less than hi - lo)
+// further on.
+MOE_HD inline int turned(int s, int rot, int lo, int hi) { return s + rot < hi ? s + rot : s + rot - (hi - lo); }
+
 // A workgroup of WT x WC waves computes 32 TB WT rows by 32 CB WC channels with
 // S stages of 128 bytes of the reduction in its ring.
 template <int TB, int CB, int WT, int WC, int S>

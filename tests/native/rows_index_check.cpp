@@ -165,7 +165,23 @@ static void norm() {
       }
 }
 
+// Each wave's part of the stages, walked from any start, is taken once.
+static void walks() {
+  for (int lo = 0; lo < 40; lo += 13)
+    for (int n = 1; n <= 40; ++n)
+      for (int rot = 0; rot < n; ++rot) {
+        std::vector<char> seen(n, 0);
+        for (int s = lo; s < lo + n; ++s) {
+          const int t = moe::turned(s, rot, lo, lo + n);
+          CHECK(t >= lo && t < lo + n, "stage %d of %d at %d", t, n, lo);
+          seen.at(t - lo)++;
+        }
+        for (char c : seen) CHECK(c == 1, "a stage of %d taken %d times", n, c);
+      }
+}
+
 int main() {
+  walks();
   for (int ks = 0; ks < 4; ++ks) no_conflicts(at32, ks);
   for (int ks = 0; ks < 2; ++ks) no_conflicts(at16, ks);
   tile<4, 2, 2, 4, 2>();
@@ -173,8 +189,10 @@ int main() {
   tile<2, 1, 2, 4, 4>();
   tile<1, 2, 2, 2, 3>();
   tile<1, 2, 1, 4, 2>();
+  tile<1, 2, 1, 4, 3>();
   tile<1, 1, 2, 2, 4>();
   rows<1, 2>();
+  rows<4, 2>();
   rows<2, 2>();
   norm();
   if (fails) {
