@@ -530,6 +530,25 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
   const bool large = a.K % 128 == 0 && reinterpret_cast<uintptr_t>(a.w) % 128 == 0 &&
                      (long long)a.E * a.N * a.K >= 128 << 20;
   const int cg = 4;  // column blocks that share their rows in an XCD's L2 (2 and 8: within 2 %; 1: 10 % slower)
+  // Few rows, where most experts fit one row block of 32 or 64 (an even routing
+  // spreads their counts by the square root of the mean, taken one and a half
+  // times; a second block reads the weights again: 30 rows each of 8 experts,
+  // 4096 x 14336: blocks of 32 109, of 64 76 us).  One workgroup a CU with a ring
+  // of three stages where a round of them is five eighths full (16 x 4096 x
+  // 49152, 192 items: 31.6, 64 x 64 39.6 us; 16 x 4096 x 32768, 128 items: 27.0
+  // and 25.4), else two with two stages where the rounds are three quarters full
+  // (16 rows each of 8 experts, 4096 x 14336, 448 items: 72 and 78 us; 7 rows each
+  // of 64 experts, 1776 x 2464, 640 items: 75 and 62 us; 50 rows each of 8 experts,
+  // 4096 x 14336: 79, 128 x 256 84 us).
+  auto fit = [&](int BM) { return avg <= BM && (a.E == 1 || 4 * (BM - avg) * (BM - avg) >= 9 * avg); };
+  const long long wide = experts * ((a.N + 255) / 256), round = 2 * cus;
+  if (wide <= cus && 8 * wide >= 5 * cus) {
+    if (fit(32)) return launch_tile<1, 2, 1, 4, 3>(a, y_bf16, cg, true, large, s);
+    if (fit(64)) return launch_tile<2, 2, 1, 4, 3>(a, y_bf16, cg, true, large, s);
+  } else if (wide > cus && 3 * ((wide + round - 1) / round * round) <= 4 * wide) {
+    if (fit(32)) return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, true, large, s);
+    if (fit(64)) return launch_tile<2, 2, 1, 4, 2>(a, y_bf16, cg, true, large, s);
+  }
   // 16384 rows of 8 experts, 4096 x 14336: 0.91, 128 x 256 1.05 ms; 128 rows each: 113 and 124 us;
   // 5565 x 2832 x 1680 (154 items, 308 of 128 x 256): 39 and 53 us
   if (avg > 112 && enough(n256, n128)) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, avg <= 192, large, s);
@@ -539,16 +558,6 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
   if (avg > 64 && 4 * n128s >= 3 * cus) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, large, s);
   // 512 x 4096 x 4096: 16.1 us, 128 x 128 17.3 us
   if (avg > 32 && 4 * items(64, 128) >= 3 * cus) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, large, s);
-  // Few rows: one workgroup a CU with a ring of three stages where a round of
-  // them is five eighths full (16 x 4096 x 49152, 192 items: 31.6, 64 x 64 39.6
-  // us; 16 x 4096 x 32768, 128 items: 27.0 and 25.4), else two with two stages
-  // where the rounds are three quarters full (16 rows each of 8 experts, 4096 x
-  // 14336, 448 items: 72 and 78 us; 7 rows each of 64 experts, 1776 x 2464, 640
-  // items: 75 and 62 us).
-  const long long n32 = items(32, 256), round = 2 * cus;
-  if (avg <= 32 && n32 <= cus && 8 * n32 >= 5 * cus) return launch_tile<1, 2, 1, 4, 3>(a, y_bf16, cg, true, large, s);
-  if (avg <= 32 && 3 * ((n32 + round - 1) / round * round) <= 4 * n32)
-    return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, true, large, s);
   // 64 x 4096 x 14336: 12 us, 64 rows on private rings 16 us; 16 x 16384 x 16384: 40, 16 rows on them 45 us
   if (4 * items(64, 64) >= 3 * cus) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, avg <= 64, large, s);
   // 16 x 14336 x 4096 (64 items of 64 channels): 11.4 us, 64 x 64 29 us

@@ -190,6 +190,8 @@ int main() {
   tile<1, 2, 2, 2, 3>();
   tile<1, 2, 1, 4, 2>();
   tile<1, 2, 1, 4, 3>();
+  tile<2, 2, 1, 4, 2>();
+  tile<2, 2, 1, 4, 3>();
   tile<1, 1, 2, 2, 4>();
   rows<1, 2>();
   rows<4, 2>();

@@ -323,3 +323,16 @@ def test_few_rows_of_wide_tiles(E, N, K, out):
     offsets, perm, T, rows = grouped(counts, 2, E)
     x, w, sx, sw = codes((T, K), K), codes((E, N, K), N), scales((T,), 1), scales((E, N), 2)
     check(run(x, sx, w, sw, offsets, perm, 2, rows, out), exact(x, sx, w, sw, offsets, perm, 2, rows), out, "y")
+
+
+# 64 x 256 tiles: experts that mostly fit one block, one and two workgroups a CU
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K", [16, 272, 1280, 2064])
+@pytest.mark.parametrize("counts,N", [([40, 64, 0, 33, 1, 70, 100, 17], 14344), ([40, 64, 0, 33, 1, 70, 100, 17], 6152), ([64], 41000),
+                                      ([33], 98312)])
+def test_mid_rows_of_wide_tiles(counts, N, K, out):
+    log(f"matmul_i8 wide tiles {counts} K={K} N={N} {out}")
+    E = len(counts)
+    offsets, perm, T, rows = grouped(counts, 2, E)
+    x, w, sx, sw = codes((T, K), K), codes((E, N, K), N), scales((T,), 1), scales((E, N), 2)
+    check(run(x, sx, w, sw, offsets, perm, 2, rows, out), exact(x, sx, w, sw, offsets, perm, 2, rows), out, "y")
