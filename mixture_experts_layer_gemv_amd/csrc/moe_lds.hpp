@@ -34,12 +34,15 @@ __device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt
 // address lds + 16 l.  The copy takes its LDS address from m0, a register the
 // compiler reserves (and may hold a value of its own in), so m0 is saved in a
 // scratch register first and restored right after the copy is issued (the
-// copy reads m0 at issue).
+// copy reads m0 at issue).  A copy into LDS needs one wait state after a scalar
+// write of m0; the compiler, which does not look into the assembly, would not
+// add it.
 __device__ __forceinline__ void copy_frag(const void* sbase, uint32_t voff, uint32_t lds) {
   uint32_t saved;
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %3\n\t"
+      "s_nop 0\n\t"
       "global_load_lds_dwordx4 %1, %2\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(saved)
