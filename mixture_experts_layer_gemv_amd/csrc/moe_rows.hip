@@ -528,7 +528,7 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
   constexpr bool FOURS = !TB || !RB;
   __shared__ float dots[4][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-  const int slabs = (A.m + 511) / 512;
+  const int slabs = row_slabs(A.m);
   for (long long i = blockIdx.x; i < A.T; i += gridDim.x) {  // the step past the last token may pass 2^31
     const int t = (int)i;
     const int mine = token_rows(A, t, lane);

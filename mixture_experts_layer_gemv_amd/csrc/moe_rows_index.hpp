@@ -30,6 +30,11 @@ MOE_HD inline NormCols slab_cols(bool fours, int lane, int slab) {
   return fours ? NormCols{at + 4 * lane, at + 256 + 4 * lane} : NormCols{at + 8 * lane, at + 8 * lane + 4};
 }
 
+// Slabs of a row.  The combine's gradient walks them with up to four waves and
+// two slabs a step: steps of 4096 columns, so that the columns past a row's end
+// stay below 2^31 too.
+MOE_HD inline int row_slabs(int m) { return (m - 1) / 512 + 1; }
+
 // Vectors of 8 per thread, and threads of a team, for rows of m.
 MOE_HD inline int norm_vecs(int m) { return m <= 8192 ? 1 : 2; }
 MOE_HD inline int norm_threads(int m) {
