@@ -515,60 +515,24 @@ hipError_t launch_matmul_i8(const I8Args& a, bool y_bf16, int cus, hipStream_t s
   if (a.R <= 0) return hipSuccess;
   if (a.K <= 0 || a.K % 16 || a.K > kI8MaxK || a.N <= 0 || a.N % 8 || a.E < 1 || (!a.offsets && a.E != 1))
     return hipErrorInvalidValue;
-  // The largest tile that still gives three quarters of the CUs an item, for
-  // experts of the mean row count: a tile reads (1 / BM + 1 / BN) bytes per
-  // product, but one round of too few tiles leaves CUs idle.  Half of the CUs
-  // are enough where the next smaller tile would need a second round.
-  const long long experts = a.R < a.E ? a.R : a.E, avg = (a.R + experts - 1) / experts;
-  auto items = [&](int BM, int BN) { return experts * ((avg + BM - 1) / BM) * ((a.N + BN - 1) / BN); };
-  auto enough = [&](long long n, long long finer) { return 4 * n >= 3 * cus || (2 * n >= cus && finer > cus); };
-  const long long n256 = items(256, 256), n128 = items(128, 256), n128s = items(128, 128);
-  // Weights that their experts' only row block reads, too large for the 256 MB
-  // last-level cache to hold until the next call, are read as not to be kept:
-  // 16 rows each of 8 experts, 470 MB: 84 -> 72 us; 16 x 28672 x 8192: 41 -> 37 us;
-  // 184 MB between other calls 37 -> 32 us (alone and warm 28.6 -> 31 us); 58 MB,
-  // warm: 10.9 -> 12.5 us.  Rows that share lines are fetched twice then (K =
-  // 1776, warm: 51 -> 62 us).
-  const bool large = a.K % 128 == 0 && reinterpret_cast<uintptr_t>(a.w) % 128 == 0 &&
-                     (long long)a.E * a.N * a.K >= 128 << 20;
+  const I8Choice c = choose_i8(a.R, a.N, a.E, cus);
+  const bool once = c.once, large = i8_weights_once(a.w, a.K, a.N, a.E);
   const int cg = 4;  // column blocks that share their rows in an XCD's L2 (2 and 8: within 2 %; 1: 10 % slower)
-  // Few rows, where most experts fit one row block of 32 or 64 (an even routing
-  // spreads their counts by the square root of the mean, taken one and a half
-  // times; a second block reads the weights again: 30 rows each of 8 experts,
-  // 4096 x 14336: blocks of 32 109, of 64 76 us).  One workgroup a CU with a ring
-  // of three stages where a round of them is five eighths full (16 x 4096 x
-  // 49152, 192 items: 31.6, 64 x 64 39.6 us; 16 x 4096 x 32768, 128 items: 27.0
-  // and 25.4), else two with two stages where the rounds are three quarters full
-  // (16 rows each of 8 experts, 4096 x 14336, 448 items: 72 and 78 us; 7 rows each
-  // of 64 experts, 1776 x 2464, 640 items: 75 and 62 us; 50 rows each of 8 experts,
-  // 4096 x 14336: 79, 128 x 256 84 us).
-  auto fit = [&](int BM) { return avg <= BM && (a.E == 1 || 4 * (BM - avg) * (BM - avg) >= 9 * avg); };
-  const long long wide = experts * ((a.N + 255) / 256), round = 2 * cus;
-  if (wide <= cus && 8 * wide >= 5 * cus) {
-    if (fit(32)) return launch_tile<1, 2, 1, 4, 3>(a, y_bf16, cg, true, large, s);
-    if (fit(64)) return launch_tile<2, 2, 1, 4, 3>(a, y_bf16, cg, true, large, s);
-  } else if (wide > cus && 3 * ((wide + round - 1) / round * round) <= 4 * wide) {
-    if (fit(32)) return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, true, large, s);
-    if (fit(64)) return launch_tile<2, 2, 1, 4, 2>(a, y_bf16, cg, true, large, s);
+  switch (c.kernel) {
+    case kTile32x256x3: return launch_tile<1, 2, 1, 4, 3>(a, y_bf16, cg, once, large, s);
+    case kTile64x256x3: return launch_tile<2, 2, 1, 4, 3>(a, y_bf16, cg, once, large, s);
+    case kTile32x256x2: return launch_tile<1, 2, 1, 4, 2>(a, y_bf16, cg, once, large, s);
+    case kTile64x256x2: return launch_tile<2, 2, 1, 4, 2>(a, y_bf16, cg, once, large, s);
+    case kTile256x256x2: return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, once, large, s);
+    case kTile128x256x3: return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, once, large, s);
+    case kTile128x128x4: return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, once, large, s);
+    case kTile64x128x3: return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, once, large, s);
+    case kTile64x64x4: return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, once, large, s);
+    case kRing16x32: return launch_rows<1, 2, 4, 2>(a, y_bf16, large, s);
+    case kRing64x32: return launch_rows<4, 2, 4, 2>(a, y_bf16, large, s);
+    case kRing32x32: return launch_rows<2, 2, 4, 2>(a, y_bf16, large, s);
+    default: return hipErrorInvalidValue;
   }
-  // 16384 rows of 8 experts, 4096 x 14336: 0.91, 128 x 256 1.05 ms; 128 rows each: 113 and 124 us;
-  // 5565 x 2832 x 1680 (154 items, 308 of 128 x 256): 39 and 53 us
-  if (avg > 112 && enough(n256, n128)) return launch_tile<4, 2, 2, 4, 2>(a, y_bf16, cg, avg <= 192, large, s);
-  // 64 rows each of 8 experts: 89, 64 x 128 106 us; 2048 x 4096 x 4096 (128 items of 256 x 256): 37 and 43 us
-  if (avg > 48 && enough(n128, n128s)) return launch_tile<2, 2, 2, 4, 3>(a, y_bf16, cg, avg <= 128, large, s);
-  // 1003 x 6400 x 4096: 33 us, 128 x 256 40 us, 64 x 128 38 us
-  if (avg > 64 && 4 * n128s >= 3 * cus) return launch_tile<2, 1, 2, 4, 4>(a, y_bf16, cg, avg <= 128, large, s);
-  // 512 x 4096 x 4096: 16.1 us, 128 x 128 17.3 us
-  if (avg > 32 && 4 * items(64, 128) >= 3 * cus) return launch_tile<1, 2, 2, 2, 3>(a, y_bf16, cg, avg <= 64, large, s);
-  // 64 x 4096 x 14336: 12 us, 64 rows on private rings 16 us; 16 x 16384 x 16384: 40, 16 rows on them 45 us
-  if (4 * items(64, 64) >= 3 * cus) return launch_tile<1, 1, 2, 2, 4>(a, y_bf16, cg, avg <= 64, large, s);
-  // 16 x 14336 x 4096 (64 items of 64 channels): 11.4 us, 64 x 64 29 us
-  if (avg <= 16) return launch_rows<1, 2, 4, 2>(a, y_bf16, large, s);
-  // 64 x 8192 x 8192 (256 items of 32 channels): 14.6 us, 32 rows 21 us; 64 x 14336 x 4096 (128): 18.4 and 13.6 us
-  if (avg > 32 && 4 * items(64, 32) >= 3 * cus) return launch_rows<4, 2, 4, 2>(a, y_bf16, large, s);
-  // 64 x 14336 x 4096: 13.6 us, 64 x 64 29.5 us; a ring of one stage for eight waves in place of two for four 13.8 us
-  // (64 x 8192 x 8192: 23 and 21 us)
-  return launch_rows<2, 2, 4, 2>(a, y_bf16, large, s);
 }
 
 }  // namespace moe

@@ -2,6 +2,8 @@
 // kernels and a host test that checks it exhaustively.  No HIP dependency.
 #pragma once
 
+#include <stdint.h>
+
 #include "moe_index.hpp"
 
 namespace moe {
@@ -108,5 +110,89 @@ struct TileShape {
 // Element v of a 32 x 32 accumulator in a lane: its channel (of 32) in steps of
 // four, the row being lane % 32.
 MOE_HD inline int acc_channel(int lane, int v) { return 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3); }
+
+// The kernels of the product, by their rows x channels x stages: tiles of a
+// workgroup's waves, and (kRing) waves with rings of their own for few rows.
+enum I8Kernel {
+  kTile32x256x3,
+  kTile64x256x3,
+  kTile32x256x2,
+  kTile64x256x2,
+  kTile256x256x2,
+  kTile128x256x3,
+  kTile128x128x4,
+  kTile64x128x3,
+  kTile64x64x4,
+  kRing16x32,
+  kRing64x32,
+  kRing32x32,
+  kI8Kernels
+};
+// once: most experts' weights are read by one row block (tiles only; rings
+// always start from different stages and look at each expert's blocks).
+struct I8Choice {
+  I8Kernel kernel;
+  bool once;
+};
+
+// The kernel for R >= 1 rows of E experts and N channels on `cus` CUs.
+//
+// The largest tile that still gives three quarters of the CUs an item, for
+// experts of the mean row count: a tile reads (1 / BM + 1 / BN) bytes per
+// product, but one round of too few tiles leaves CUs idle.  Half of the CUs
+// are enough where the next smaller tile would need a second round.
+inline I8Choice choose_i8(int R, int N, int E, int cus) {
+  const long long experts = R < E ? R : E, avg = (R + experts - 1) / experts;
+  auto items = [&](int BM, int BN) { return experts * ((avg + BM - 1) / BM) * ((N + BN - 1) / BN); };
+  auto enough = [&](long long n, long long finer) { return 4 * n >= 3 * cus || (2 * n >= cus && finer > cus); };
+  const long long n256 = items(256, 256), n128 = items(128, 256), n128s = items(128, 128);
+  // Few rows, where most experts fit one row block of 32 or 64 (an even routing
+  // spreads their counts by the square root of the mean, taken one and a half
+  // times; a second block reads the weights again: 30 rows each of 8 experts,
+  // 4096 x 14336: blocks of 32 109, of 64 76 us).  One workgroup a CU with a ring
+  // of three stages where a round of them is five eighths full (16 x 4096 x
+  // 49152, 192 items: 31.6, 64 x 64 39.6 us; 16 x 4096 x 32768, 128 items: 27.0
+  // and 25.4), else two with two stages where the rounds are three quarters full
+  // (16 rows each of 8 experts, 4096 x 14336, 448 items: 72 and 78 us; 7 rows each
+  // of 64 experts, 1776 x 2464, 640 items: 75 and 62 us; 50 rows each of 8 experts,
+  // 4096 x 14336: 79, 128 x 256 84 us).
+  auto fit = [&](int BM) { return avg <= BM && (E == 1 || 4 * (BM - avg) * (BM - avg) >= 9 * avg); };
+  const long long wide = experts * ((N + 255) / 256), round = 2LL * cus;
+  if (wide <= cus && 8 * wide >= 5 * cus) {
+    if (fit(32)) return {kTile32x256x3, true};
+    if (fit(64)) return {kTile64x256x3, true};
+  } else if (wide > cus && 3 * ((wide + round - 1) / round * round) <= 4 * wide) {
+    if (fit(32)) return {kTile32x256x2, true};
+    if (fit(64)) return {kTile64x256x2, true};
+  }
+  // 16384 rows of 8 experts, 4096 x 14336: 0.91, 128 x 256 1.05 ms; 128 rows each: 113 and 124 us;
+  // 5565 x 2832 x 1680 (154 items, 308 of 128 x 256): 39 and 53 us
+  if (avg > 112 && enough(n256, n128)) return {kTile256x256x2, avg <= 192};
+  // 64 rows each of 8 experts: 89, 64 x 128 106 us; 2048 x 4096 x 4096 (128 items of 256 x 256): 37 and 43 us
+  if (avg > 48 && enough(n128, n128s)) return {kTile128x256x3, avg <= 128};
+  // 1003 x 6400 x 4096: 33 us, 128 x 256 40 us, 64 x 128 38 us
+  if (avg > 64 && 4 * n128s >= 3 * cus) return {kTile128x128x4, avg <= 128};
+  // 512 x 4096 x 4096: 16.1 us, 128 x 128 17.3 us
+  if (avg > 32 && 4 * items(64, 128) >= 3 * cus) return {kTile64x128x3, avg <= 64};
+  // 64 x 4096 x 14336: 12 us, 64 rows on private rings 16 us; 16 x 16384 x 16384: 40, 16 rows on them 45 us
+  if (4 * items(64, 64) >= 3 * cus) return {kTile64x64x4, avg <= 64};
+  // 16 x 14336 x 4096 (64 items of 64 channels): 11.4 us, 64 x 64 29 us
+  if (avg <= 16) return {kRing16x32, true};
+  // 64 x 8192 x 8192 (256 items of 32 channels): 14.6 us, 32 rows 21 us; 64 x 14336 x 4096 (128): 18.4 and 13.6 us
+  if (avg > 32 && 4 * items(64, 32) >= 3 * cus) return {kRing64x32, true};
+  // 64 x 14336 x 4096: 13.6 us, 64 x 64 29.5 us; a ring of one stage for eight waves in place of two for four 13.8 us
+  // (64 x 8192 x 8192: 23 and 21 us)
+  return {kRing32x32, true};
+}
+
+// Weights that their experts' only row block reads, too large for the 256 MB
+// last-level cache to hold until the next call, are read as not to be kept:
+// 16 rows each of 8 experts, 470 MB: 84 -> 72 us; 16 x 28672 x 8192: 41 -> 37 us;
+// 184 MB between other calls 37 -> 32 us (alone and warm 28.6 -> 31 us); 58 MB,
+// warm: 10.9 -> 12.5 us.  Rows that share lines (w off 128 bytes, or K) are
+// fetched twice then (K = 1776, warm: 51 -> 62 us).
+inline bool i8_weights_once(const void* w, int K, int N, int E) {
+  return K % 128 == 0 && reinterpret_cast<uintptr_t>(w) % 128 == 0 && (long long)E * N * K >= 128 << 20;
+}
 
 }  // namespace moe
