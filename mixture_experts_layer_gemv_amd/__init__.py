@@ -238,20 +238,33 @@ def moe_quantize_rows_i8(x, T, m, xq, scale, stream=None):
     _check("moe_quantize_rows_i8", lib().moe_quantize_rows_i8(_p(x), T, m, _p(xq), _p(scale), _s(stream)))
 
 
+_elements = None  # {value type, _INDEX or _CODE: the torch types of its elements}
+_INDEX, _CODE = "int32 indices", "int8 codes"
+
+
 def _tensors(fn, *sized):
     """The row operators' tensor arguments as device pointers, each given with
-    the bytes the call reads or writes there; a tensor that is not on the
-    current GPU, not contiguous, too small or of 64-bit elements (torch's own
-    indices: the calls take int32) raises before the call."""
+    the bytes the call reads or writes there and what they hold (a value type,
+    _INDEX, _CODE, or None for a workspace); a tensor that is not on the current
+    GPU, not contiguous, too small or of other elements raises before the call.
+    bf16 may come as its bit patterns in 16-bit integers; pointers pass as they are."""
+    global _elements
+    if _elements is None:
+        torch = _torch()
+        _elements = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                     _INDEX: (torch.int32,), _CODE: (torch.int8,)}
     out, dev = [], -1
-    for t, nbytes in sized:
+    for t, nbytes, kind in sized:
         if t is not None and type(t) is not int:
             d = t.get_device()  # -1: not on a GPU
             if dev < 0 <= d:
                 dev = _torch().cuda.current_device()
-            if d < 0 or d != dev or t.nbytes < nbytes or t.itemsize > 4 or not t.is_contiguous():
+            # (the call refuses a value type that is not in the table)
+            if d < 0 or d != dev or t.nbytes < nbytes or not t.is_contiguous() or \
+                    (kind in _elements and t.dtype not in _elements[kind]):
+                need = {MOE_F32: "fp32", MOE_BF16: "bf16"}.get(kind, kind)
                 raise MoeError(fn, MOE_ERR_INVALID_ARG, f"{t.dtype} tensor {tuple(t.shape)} on {t.device}: need "
-                               f"{nbytes} contiguous bytes of at most 32-bit elements on the current GPU")
+                               f"{nbytes} contiguous bytes{f' of {need}' if kind in _elements else ''} on the current GPU")
             t = t.data_ptr()
         out.append(t)
     return out
@@ -264,8 +277,9 @@ def _size(dtype):
 
 def moe_norm_forward(x, dtype, norm, gamma, beta, eps, T, m, y, mean=None, rstd=None, stream=None):
     n = T * m * _size(dtype)
-    x, gamma, beta, y, mean, rstd = _tensors("moe_norm_forward", (x, n), (gamma, 4 * m), (beta, 4 * m), (y, n),
-                                             (mean, 4 * T), (rstd, 4 * T))
+    x, gamma, beta, y, mean, rstd = _tensors("moe_norm_forward", (x, n, dtype), (gamma, 4 * m, MOE_F32),
+                                             (beta, 4 * m, MOE_F32), (y, n, dtype), (mean, 4 * T, MOE_F32),
+                                             (rstd, 4 * T, MOE_F32))
     _check("moe_norm_forward", lib().moe_norm_forward(x, dtype, norm, gamma, beta, eps, T, m, y, mean, rstd,
                                                       _s(stream)))
 
@@ -280,28 +294,31 @@ def moe_norm_backward(dy, x, dtype, norm, gamma, mean, rstd, T, m, dx, dgamma, d
                       stream=None):
     n = T * m * _size(dtype)
     dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace = _tensors(
-        "moe_norm_backward", (dy, n), (x, n), (gamma, 4 * m), (mean, 4 * T), (rstd, 4 * T), (dx, n), (dgamma, 4 * m),
-        (dbeta, 4 * m), (workspace, ws_bytes))
+        "moe_norm_backward", (dy, n, dtype), (x, n, dtype), (gamma, 4 * m, MOE_F32), (mean, 4 * T, MOE_F32),
+        (rstd, 4 * T, MOE_F32), (dx, n, dtype), (dgamma, 4 * m, MOE_F32), (dbeta, 4 * m, MOE_F32),
+        (workspace, ws_bytes, None))
     _check("moe_norm_backward", lib().moe_norm_backward(dy, x, dtype, norm, gamma, mean, rstd, T, m, dx, dgamma, dbeta,
                                                         workspace, ws_bytes, _s(stream)))
 
 
 def moe_permute_rows(x, dtype, inv_perm, T, m, k, rows, x_perm, stream=None):
     e = m * _size(dtype)
-    x, inv_perm, x_perm = _tensors("moe_permute_rows", (x, T * e), (inv_perm, 4 * T * k), (x_perm, rows * e))
+    x, inv_perm, x_perm = _tensors("moe_permute_rows", (x, T * e, dtype), (inv_perm, 4 * T * k, _INDEX),
+                                   (x_perm, rows * e, dtype))
     _check("moe_permute_rows", lib().moe_permute_rows(x, dtype, inv_perm, T, m, k, rows, x_perm, _s(stream)))
 
 
 def moe_permute_rows_backward(dx_perm, row_dtype, inv_perm, T, m, k, rows, dx, x_dtype, stream=None):
-    dx_perm, inv_perm, dx = _tensors("moe_permute_rows_backward", (dx_perm, rows * m * _size(row_dtype)),
-                                     (inv_perm, 4 * T * k), (dx, T * m * _size(x_dtype)))
+    dx_perm, inv_perm, dx = _tensors("moe_permute_rows_backward", (dx_perm, rows * m * _size(row_dtype), row_dtype),
+                                     (inv_perm, 4 * T * k, _INDEX), (dx, T * m * _size(x_dtype), x_dtype))
     _check("moe_permute_rows_backward", lib().moe_permute_rows_backward(dx_perm, row_dtype, inv_perm, T, m, k, rows,
                                                                         dx, x_dtype, _s(stream)))
 
 
 def moe_combine_rows(y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, y, y_dtype, stream=None):
-    y_perm, inv_perm, topk_w, y = _tensors("moe_combine_rows", (y_perm, rows * m * _size(row_dtype)),
-                                           (inv_perm, 4 * T * k), (topk_w, 4 * T * k), (y, T * m * _size(y_dtype)))
+    y_perm, inv_perm, topk_w, y = _tensors("moe_combine_rows", (y_perm, rows * m * _size(row_dtype), row_dtype),
+                                           (inv_perm, 4 * T * k, _INDEX), (topk_w, 4 * T * k, MOE_F32),
+                                           (y, T * m * _size(y_dtype), y_dtype))
     _check("moe_combine_rows", lib().moe_combine_rows(y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, y, y_dtype,
                                                       _s(stream)))
 
@@ -310,21 +327,24 @@ def moe_combine_rows_backward(dy, dy_dtype, y_perm, row_dtype, inv_perm, topk_w,
                               stream=None):
     r = rows * m * _size(row_dtype)
     dy, y_perm, inv_perm, topk_w, dy_perm, d_topk_w = _tensors(
-        "moe_combine_rows_backward", (dy, T * m * _size(dy_dtype)), (y_perm, r), (inv_perm, 4 * T * k),
-        (topk_w, 4 * T * k), (dy_perm, r), (d_topk_w, 4 * T * k))
+        "moe_combine_rows_backward", (dy, T * m * _size(dy_dtype), dy_dtype), (y_perm, r, row_dtype),
+        (inv_perm, 4 * T * k, _INDEX), (topk_w, 4 * T * k, MOE_F32), (dy_perm, r, row_dtype),
+        (d_topk_w, 4 * T * k, MOE_F32))
     _check("moe_combine_rows_backward", lib().moe_combine_rows_backward(
         dy, dy_dtype, y_perm, row_dtype, inv_perm, topk_w, T, m, k, rows, dy_perm, d_topk_w, _s(stream)))
 
 
 def moe_quantize_codes_i8(x, T, m, codes, scale, stream=None):
-    x, codes, scale = _tensors("moe_quantize_codes_i8", (x, 2 * T * m), (codes, T * m), (scale, 4 * T))
+    x, codes, scale = _tensors("moe_quantize_codes_i8", (x, 2 * T * m, MOE_BF16), (codes, T * m, _CODE),
+                               (scale, 4 * T, MOE_F32))
     _check("moe_quantize_codes_i8", lib().moe_quantize_codes_i8(x, T, m, codes, scale, _s(stream)))
 
 
 def moe_matmul_i8(x, x_scale, w, w_scale, offsets, perm, T, topk, rows, K, N, E, y, y_dtype, stream=None):
     x, x_scale, w, w_scale, offsets, perm, y = _tensors(
-        "moe_matmul_i8", (x, T * K), (x_scale, 4 * T), (w, E * N * K), (w_scale, 4 * E * N), (offsets, 4 * (E + 1)),
-        (perm, 4 * rows), (y, rows * N * _size(y_dtype)))
+        "moe_matmul_i8", (x, T * K, _CODE), (x_scale, 4 * T, MOE_F32), (w, E * N * K, _CODE),
+        (w_scale, 4 * E * N, MOE_F32), (offsets, 4 * (E + 1), _INDEX), (perm, 4 * rows, _INDEX),
+        (y, rows * N * _size(y_dtype), y_dtype))
     _check("moe_matmul_i8", lib().moe_matmul_i8(x, x_scale, w, w_scale, offsets, perm, T, topk, rows, K, N, E, y,
                                                 y_dtype, _s(stream)))
 
