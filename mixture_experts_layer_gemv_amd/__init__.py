@@ -136,11 +136,26 @@ def _p(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
+def _stream_getter():
+    """A function that gives torch's current stream as a handle: without building
+    a Stream object (8.8 -> 5.9 us for the shortest calls) where torch has the
+    function for that, which is not a public one."""
+    torch = _torch()
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
 def _s(stream):
+    global _current_stream
     if stream is None:
-        torch = _torch()
-        # torch.cuda.current_stream().cuda_stream without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _current_stream is None:
+            _current_stream = _stream_getter()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
