@@ -405,7 +405,8 @@ moe_status moe_layer_forward_noalloc(const moe_weights* w, const float* w_router
  * steps next to moe_dispatch and the experts for a caller that trains
  * through them or runs products of its own on the dispatched rows.  They
  * share the conventions above, with these limits: m and N multiples of 8, m
- * <= 16384 for the norms, K a multiple of 16, outputs overlapping no input.
+ * <= 16384 for the norms, K a multiple of 16, outputs overlapping no input
+ * except where said.
  * Sums and statistics are fp32 (int32 in the product); each output is rounded
  * once.  No result depends on the timing of workgroups.
  */
@@ -481,6 +482,7 @@ moe_status moe_permute_rows_backward(const void* dx_perm, int row_dtype, const i
  *  topk_w, d_topk_w device fp32 [T][k].
  *  dy_perm, d_topk_w  one of them may be NULL (without d_topk_w, y_perm may be NULL too).
  *                   Rows of dy_perm that no entry of inv_perm names are left as they were.
+ *                   dy_perm may be y_perm itself: each element is read before it is written.
  * Errors: INVALID_ARG, UNSUPPORTED, HIP.
  */
 moe_status moe_combine_rows(const void* y_perm, int row_dtype, const int32_t* inv_perm, const float* topk_w, int T, int m,

@@ -522,6 +522,8 @@ __global__ __launch_bounds__(256) void k_combine_rows(const RowsArgs A, int slic
 
 // The combine's gradient, one block of up to four waves per token:
 // out[inv[t*k+j]] = w[t,j] dy[t], dw[t,j] = <dy[t], rows[inv[t*k+j]]>.
+// out may be rows: a lane writes the columns that it has read itself (lanes past
+// the row's end read columns of others and drop them).
 template <bool TB, bool RB, bool ONCE>
 __global__ __launch_bounds__(256) void k_combine_rows_bwd(const RowsArgs A) {
   constexpr int V = 2;
