@@ -509,7 +509,8 @@ moe_status moe_quantize_codes_i8(const void* x, int T, int m, int8_t* codes, flo
  * experts' row ranges of a dispatch:
  *   y[r][n] = x_scale[t] * w_scale[e][n] * sum_{i<K} x[t][i] * w[e][n][i]
  * for every row r of expert e (offsets[e] <= r < offsets[e+1]), t = perm[r] / topk
- * (so x stays in token order) or t = r without perm.  The sum is exact in int32.
+ * (so x stays in token order) or t = r without perm.  The sum is exact in int32; in
+ * fp32 it is multiplied by x_scale first, a product that has to stay in fp32's range.
  *  x          device int8 [T][K].       x_scale  device fp32 [T].
  *  w          device int8 [E][N][K]: each output channel's K codes together
  *             (w1 and w2 of moe_weights_create are [E][K][N]).

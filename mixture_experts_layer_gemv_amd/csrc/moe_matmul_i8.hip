@@ -146,8 +146,9 @@ void dispatch(F go, bool y_bf16, bool nt) {
 // its W waves split the reduction and add their int32 sums in LDS.  Each wave
 // copies its own lines through a private ring of S stages (128 bytes of every
 // row and channel), so no wave waits for another before the final sum.  The
-// weights' bytes bound it: 16 x 14336 x 4096 takes 11.3 us, 5.2 TB/s, and 16 x
-// 28672 x 8192 37 us, 6.3 TB/s (a large copy reaches 5.0 on this card).  Weights
+// weights' bytes bound it: 16 x 28672 x 8192 takes 38 us, 6.2 TB/s (a large copy
+// reaches 5.0 on this card), 16 x 14336 x 4096 17.9 us, 3.3 TB/s, and with its
+// weights in the last-level cache 11.6 us.  Weights
 // loaded straight into registers, half a line an instruction, took 13.5 us
 // where these copies took 11.1 (16 x 4096 x 14336).  Neighbouring workgroups
 // start from different stages, see k_i8_tile (16 x 16384 x 8192: 31 against 24 us).
@@ -284,7 +285,7 @@ hipError_t launch_rows(const I8Args& a, bool y_bf16, bool large, hipStream_t s) 
 //
 // What bounds it: large products (256 x 256 tiles, two waves per SIMD, 128 x
 // 64 each) the power of products, LDS reads and copies together.  8192 x 4096
-// x 14336 takes 408 us, 2.36 POP/s; the products alone 283 us, products and
+// x 14336 takes 408 to 418 us, 2.3 POP/s; the products alone 283 us, products and
 // LDS reads 350 us, the copies alone 290 us, while the clock falls to 1.8 GHz.
 // A deeper ring (96 KiB under way instead of 64) and four waves of 128 x 128
 // (a third fewer LDS reads) measured 2 and 3 % slower.  Products of few rows

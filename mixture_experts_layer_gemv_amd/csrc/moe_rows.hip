@@ -8,7 +8,7 @@
 // parentheses the algorithmic bytes over the time (a large copy reaches 5.0
 // TB/s on this card): layer norm 24.5 us (5.5 TB/s), its gradients 41.4 us (4.9),
 // top-2 permute 38.4 us (5.2), its gradient and the combine 34.5 us (5.8), the
-// combine's gradient 66.0 us (5.1).
+// combine's gradient 66.4 us (5.1).
 #include <type_traits>
 
 #include "moe_kernels.hpp"
@@ -260,7 +260,11 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
     nmu = LAYER ? A.mean[row] : 0.0f;
     nr = A.rstd[row];
   };
-  constexpr bool AHEAD = V == 1;  // the next row loaded during this one's sums: with V = 2 there are no registers for it
+  // The next row loaded during this one's sums.  With V = 2 it takes 16 (bf16) or
+  // 32 registers, and of the 128 that 1024 threads leave a thread 104 (RMS, bf16)
+  // to 128 (layer norm, fp32) are in use: there is room for it in the bf16 RMS
+  // form only, which has no form of its own.
+  constexpr bool AHEAD = V == 1;
   const long long stride = (long long)gridDim.x * teams;
   if (AHEAD) fetch((long long)blockIdx.x * teams + team);
   int turn = 0;

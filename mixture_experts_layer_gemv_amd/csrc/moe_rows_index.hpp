@@ -129,7 +129,17 @@ enum I8Kernel {
   kI8Kernels
 };
 // once: most experts' weights are read by one row block (tiles only; rings
-// always start from different stages and look at each expert's blocks).
+// always start from different stages and look at each expert's blocks).  Then
+// neighbouring tiles start from different stages, and large weights are not
+// kept.  Its limits are a mean of three quarters of the 256-row block and of all
+// of a smaller one.  Measured with once and without, weights from HBM (E * N * K
+// of 600 MB or more in turn), 8 experts of so many rows in the mean: 256 x 256
+// tiles, 4096 x 8192: 128 rows 61 and 78 us, 192 67 and 81, 224 75 and 84, 256 115
+// and 121, 300 111 and 114; 256 dense rows, 8192 x 57344: 128 and 145; 128 x 128,
+// 4096 x 4096: 96 rows 36 and 39, 128 50 and 51; 128 x 256, the same: 160 rows 42
+// and 44; 64 x 128, 4096 x 3328: 40 rows 25 and 31, 64 37 and 40; 64 x 64: 70 dense
+// rows, 16384 x 8192: 38.6 and 40.1.  So it still gains 2 to 12 % past the limits,
+// which are on the low side.
 struct I8Choice {
   I8Kernel kernel;
   bool once;
