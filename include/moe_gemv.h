@@ -530,6 +530,138 @@ moe_status moe_matmul_i8(const int8_t* x, const float* x_scale, const int8_t* w,
                          void* y, int y_dtype, void* stream);
 
 /*
+ * ---- A trainable block ------------------------------------------------------
+ *
+ * What a training step runs before and between the row operators above: the
+ * residual's addition with the norm that follows it, the experts on plain weights
+ * with all gradients, and the routing's gradient.  One step of a block:
+ *   moe_add_norm_forward -> moe_route_topk -> moe_dispatch ->
+ *   moe_gated_ffn_forward -> moe_combine_rows, and back
+ *   moe_combine_rows_backward -> moe_gated_ffn_backward ->
+ *   moe_permute_rows_backward -> moe_route_backward -> moe_add_norm_backward.
+ * Conventions and limits as above: m and p multiples of 8; sums and statistics
+ * in fp32, each output rounded once, and no result depends on the timing of
+ * workgroups.  Every call may be captured into a graph; a workspace serves one
+ * call (or one replay of one graph) at a time.
+ */
+
+/*
+ * moe_add_norm_forward -- a block's input: the residual added, the norm of the
+ * sum (moe_norm_forward's) and, for moe_matmul_i8, its int8 codes (the fused
+ * region "bias and residual add" with the norm, and the INT8 GeMM's activations,
+ * of the DeepSpeed-Inference summary, datalearner.com, section 4):
+ *   s[t] = x[t] + residual[t];   y[t] = norm(s[t]);
+ *   scale[t] = 2^X, X the smallest integer with max_i |y[t][i]| <= 127 * 2^X;
+ *   codes[t][i] = round-half-even(y[t][i] / scale[t])
+ * The norm takes the fp32 sum and the codes the fp32 y, not their rounded values.
+ *  x          device [T][m] in dtype (MOE_F32 or MOE_BF16).
+ *  residual   device [T][m] in dtype, or NULL (then s is x).
+ *  norm, gamma, beta, eps, mean, rstd   as in moe_norm_forward.
+ *  sum        device [T][m] in dtype: s, or NULL.  sum and y may be x or residual
+ *             themselves, but not the same rows.
+ *  y          device [T][m] in dtype, or NULL with codes.
+ *  codes      device int8 [T][m] or NULL, with scale, device fp32 [T].  Finite rows;
+ *             codes of a row that holds other values are unspecified.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+moe_status moe_add_norm_forward(const void* x, const void* residual, int dtype, int norm, const float* gamma,
+                                const float* beta, float eps, int T, int m, void* sum, void* y, int8_t* codes,
+                                float* scale, float* mean, float* rstd, void* stream);
+
+/*
+ * moe_add_norm_backward -- its gradient, the same for x and residual:
+ *   dx = dsum + (moe_norm_backward's dx of sum)
+ *  dsum       device [T][m] in dtype: the gradient that reaches s itself (the
+ *             residual stream's), or NULL.
+ *  sum        device [T][m] in dtype, as moe_add_norm_forward left it.
+ *  dx         may be dsum or dy itself.
+ * Other arguments, workspace and errors as moe_norm_backward
+ * (moe_norm_backward_workspace_size).
+ */
+moe_status moe_add_norm_backward(const void* dy, const void* dsum, const void* sum, int dtype, int norm,
+                                 const float* gamma, const float* mean, const float* rstd, int T, int m, void* dx,
+                                 float* dgamma, float* dbeta, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * moe_gated_ffn_forward -- the SwiGLU experts of moe_expert_ffn on weights as
+ * they lie, dense or over the experts' row ranges of a dispatch, keeping what the
+ * gradient needs (HARMOEny article, section 3.2: the expert is x*W1*W2).  For
+ * every row r of expert e (offsets[e] <= r < offsets[e+1]), t = perm[r] / topk or
+ * t = r without perm:
+ *   g = x[t] w_gate[e];  u = x[t] w_up[e];  y_perm[r] = (SiLU(g) * u) w_down[e]
+ * The hidden row SiLU(g) * u is rounded to dtype between the projections.
+ *  x          device [T][m] in dtype (MOE_F32 or MOE_BF16), as all tensors here.
+ *  w_gate, w_up   device [E][m][p].   w_down  device [E][p][m].  (moe_weights_create's w1, w_up, w2.)
+ *  offsets    device int32 [E+1] from moe_dispatch, or NULL: E must be 1 and all rows
+ *             are its.  Values are read as if clamped to [0, rows], a decreasing one
+ *             as its predecessor; rows of no range are left as they were.
+ *  perm       device int32 [rows] from moe_dispatch, or NULL (T must equal rows).
+ *             perm[r] / topk is read as if clamped to [0, T).
+ *  y_perm     device [rows][m].
+ *  gate, up   device [rows][p]: g and u, or both NULL.
+ *  workspace  device, 256-byte aligned, at least moe_gated_ffn_workspace_size(dtype,
+ *             rows, m, p, E, 0) bytes.
+ *  m, p <= 2^20; 1 <= E <= 64; (rows / 64 + E) * ceil(max(m, p) / 128) < 2^22;
+ *  3 * E * ceil(m / 128) * ceil(p / 128) < 2^23.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.
+ */
+moe_status moe_gated_ffn_workspace_size(int dtype, int rows, int m, int p, int E, int backward, size_t* bytes);
+moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, const void* w_up, const void* w_down,
+                                 const int32_t* offsets, const int32_t* perm, int T, int topk, int rows, int m, int p,
+                                 int E, void* y_perm, void* gate, void* up, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/*
+ * moe_gated_ffn_backward -- its gradients.  With s = sigmoid(g), h = g s u and
+ * dh[r] = dy_perm[r] w_down[e]^T:
+ *   dg = dh u s (1 + g (1 - s)),   du = dh g s
+ *   dx_perm[r] = dg w_gate[e]^T + du w_up[e]^T
+ *   dw_gate[e] = sum_r x[t]^T dg,  dw_up[e] = sum_r x[t]^T du,  dw_down[e] = sum_r h^T dy_perm[r]
+ * dh stays in fp32; dg, du and h are rounded to dtype as operands of the products.
+ *  dy_perm    device [rows][m];  gate, up as moe_gated_ffn_forward left them.
+ *  x, weights, offsets, perm and sizes   as there (x may be NULL without dw_gate).
+ *  dx_perm    device [rows][m] or NULL; moe_permute_rows_backward sums it to the
+ *             tokens.  Rows of no range are left as they were.  May be dy_perm itself.
+ *  dw_gate, dw_up   device [E][m][p], or both NULL.   dw_down  device [E][p][m] or NULL.
+ *             Overwritten; zeros for an expert without rows.
+ *  workspace  as there, with backward = 1.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.
+ */
+moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype, const void* w_gate, const void* w_up,
+                                  const void* w_down, const void* gate, const void* up, const int32_t* offsets,
+                                  const int32_t* perm, int T, int topk, int rows, int m, int p, int E, void* dx_perm,
+                                  void* dw_gate, void* dw_up, void* dw_down, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/*
+ * moe_route_backward -- the gradient of moe_route_topk's gate weights, through
+ * the softmax over the chosen logits and the router product:
+ *   d_logits[t][e] = d_logits_add[t][e] + sum over j with topk_idx[t][j] = e of
+ *                    topk_w[t][j] * (d_topk_w[t][j] - sum_i topk_w[t][i] d_topk_w[t][i])
+ *   dx[t] = dx_add[t] + d_logits[t] w_router^T
+ *   dw_router = sum_t x[t]^T d_logits[t],   db_router = sum_t d_logits[t]
+ *  d_topk_w, topk_w   device fp32 [T][k];  topk_idx  device int32 [T][k] (an index
+ *             outside [0, E) reaches no logit).
+ *  d_logits_add   device fp32 [T][E] or NULL: the gradient of a loss on the logits
+ *             themselves (load balancing).
+ *  x          device [T][m] in x_dtype (may be NULL without dw_router).
+ *  w_router   device fp32 [m][E] (may be NULL without dx).
+ *  dx_add     device [T][m] in x_dtype or NULL: the gradient that reaches x by
+ *             another way (the experts' rows, moe_permute_rows_backward).
+ *  d_logits   device fp32 [T][E] output.   dx  device [T][m] in x_dtype or NULL; may be dx_add itself.
+ *  dw_router  device fp32 [m][E] or NULL.  db_router  device fp32 [E] or NULL.  Overwritten, with zeros when T is 0.
+ *  workspace  with dw_router or db_router: device, 256-byte aligned, at least
+ *             moe_route_backward_workspace_size(T, m, E) bytes.  Else NULL.
+ *  m a multiple of 8, <= 2^20.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.
+ */
+moe_status moe_route_backward_workspace_size(int T, int m, int E, size_t* bytes);
+moe_status moe_route_backward(const float* d_topk_w, const int32_t* topk_idx, const float* topk_w,
+                              const float* d_logits_add, const void* x, int x_dtype, const float* w_router,
+                              const void* dx_add, int T, int m, int E, int k, float* d_logits, void* dx,
+                              float* dw_router, float* db_router, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Measurement aid (not part of the layer).  Between moe_profile_begin and
  * moe_profile_end every kernel the library launches is bracketed by HIP
  * events on its own stream.  moe_profile_end waits for the last event and
@@ -539,7 +671,9 @@ moe_status moe_matmul_i8(const int8_t* x, const float* x_scale, const int8_t* w,
  * not timed).  Kernel names: "route_topk", "dispatch", "ffn_up", "ffn_down",
  * "ffn_f32_up", "ffn_f32_down", "combine", "finalize", "fill"; of the row
  * operators "norm_fwd", "norm_bwd", "permute_rows", "permute_rows_bwd",
- * "combine_rows", "combine_rows_bwd", "quant_rows", "matmul_i8".
+ * "combine_rows", "combine_rows_bwd", "quant_rows", "matmul_i8"; of the trainable
+ * block "add_norm_fwd", "add_norm_bwd", "gated_up", "gated_down",
+ * "gated_grad_hidden", "gather_rows", "gated_grad_w", "gated_grad_x", "route_bwd".
  */
 moe_status moe_profile_begin(int max_launches);
 moe_status moe_profile_end(void);

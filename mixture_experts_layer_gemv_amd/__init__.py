@@ -85,6 +85,18 @@ _SIGS = {
     "moe_combine_rows_backward": ([_vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp], _i32),
     "moe_quantize_codes_i8": ([_vp, _i32, _i32, _vp, _vp, _vp], _i32),
     "moe_matmul_i8": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp], _i32),
+    "moe_add_norm_forward": ([_vp, _vp, _i32, _i32, _vp, _vp, ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _vp], _i32),
+    "moe_add_norm_backward": ([_vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp],
+                              _i32),
+    "moe_gated_ffn_workspace_size": ([_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)], _i32),
+    "moe_gated_ffn_forward": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                               _vp, _sz, _vp], _i32),
+    "moe_gated_ffn_backward": ([_vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "moe_route_backward_workspace_size": ([_i32, _i32, _i32, ctypes.POINTER(_sz)], _i32),
+    "moe_route_backward": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                            _sz, _vp], _i32),
     "moe_layer_forward": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _sz,
                            _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "moe_layer_forward_fused": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _i32,
@@ -362,6 +374,81 @@ def moe_matmul_i8(x, x_scale, w, w_scale, offsets, perm, T, topk, rows, K, N, E,
         (y, rows * N * _size(y_dtype), y_dtype))
     _check("moe_matmul_i8", lib().moe_matmul_i8(x, x_scale, w, w_scale, offsets, perm, T, topk, rows, K, N, E, y,
                                                 y_dtype, _s(stream)))
+
+
+def moe_add_norm_forward(x, residual, dtype, norm, gamma, beta, eps, T, m, sum, y, codes=None, scale=None, mean=None,
+                         rstd=None, stream=None):
+    n = T * m * _size(dtype)
+    x, residual, gamma, beta, sum, y, codes, scale, mean, rstd = _tensors(
+        "moe_add_norm_forward", (x, n, dtype), (residual, n, dtype), (gamma, 4 * m, MOE_F32), (beta, 4 * m, MOE_F32),
+        (sum, n, dtype), (y, n, dtype), (codes, T * m, _CODE), (scale, 4 * T, MOE_F32), (mean, 4 * T, MOE_F32),
+        (rstd, 4 * T, MOE_F32))
+    _check("moe_add_norm_forward", lib().moe_add_norm_forward(x, residual, dtype, norm, gamma, beta, eps, T, m, sum, y,
+                                                              codes, scale, mean, rstd, _s(stream)))
+
+
+def moe_add_norm_backward(dy, dsum, sum, dtype, norm, gamma, mean, rstd, T, m, dx, dgamma, dbeta, workspace=None,
+                          ws_bytes=0, stream=None):
+    n = T * m * _size(dtype)
+    dy, dsum, sum, gamma, mean, rstd, dx, dgamma, dbeta, workspace = _tensors(
+        "moe_add_norm_backward", (dy, n, dtype), (dsum, n, dtype), (sum, n, dtype), (gamma, 4 * m, MOE_F32),
+        (mean, 4 * T, MOE_F32), (rstd, 4 * T, MOE_F32), (dx, n, dtype), (dgamma, 4 * m, MOE_F32),
+        (dbeta, 4 * m, MOE_F32), (workspace, ws_bytes, None))
+    _check("moe_add_norm_backward", lib().moe_add_norm_backward(dy, dsum, sum, dtype, norm, gamma, mean, rstd, T, m, dx,
+                                                                dgamma, dbeta, workspace, ws_bytes, _s(stream)))
+
+
+def moe_gated_ffn_workspace_size(dtype, rows, m, p, E, backward) -> int:
+    n = _sz()
+    _check("moe_gated_ffn_workspace_size", lib().moe_gated_ffn_workspace_size(dtype, rows, m, p, E, int(backward),
+                                                                              ctypes.byref(n)))
+    return n.value
+
+
+def moe_gated_ffn_forward(x, dtype, w_gate, w_up, w_down, offsets, perm, T, topk, rows, m, p, E, y_perm, gate=None,
+                          up=None, workspace=None, ws_bytes=0, stream=None):
+    e = _size(dtype)
+    w, hidden = E * m * p * e, rows * p * e
+    x, w_gate, w_up, w_down, offsets, perm, y_perm, gate, up, workspace = _tensors(
+        "moe_gated_ffn_forward", (x, T * m * e, dtype), (w_gate, w, dtype), (w_up, w, dtype), (w_down, w, dtype),
+        (offsets, 4 * (E + 1), _INDEX), (perm, 4 * rows, _INDEX), (y_perm, rows * m * e, dtype), (gate, hidden, dtype),
+        (up, hidden, dtype), (workspace, ws_bytes, None))
+    _check("moe_gated_ffn_forward", lib().moe_gated_ffn_forward(x, dtype, w_gate, w_up, w_down, offsets, perm, T, topk,
+                                                                rows, m, p, E, y_perm, gate, up, workspace, ws_bytes,
+                                                                _s(stream)))
+
+
+def moe_gated_ffn_backward(dy_perm, x, dtype, w_gate, w_up, w_down, gate, up, offsets, perm, T, topk, rows, m, p, E,
+                           dx_perm, dw_gate, dw_up, dw_down, workspace=None, ws_bytes=0, stream=None):
+    e = _size(dtype)
+    w, hidden, r = E * m * p * e, rows * p * e, rows * m * e
+    dy_perm, x, w_gate, w_up, w_down, gate, up, offsets, perm, dx_perm, dw_gate, dw_up, dw_down, workspace = _tensors(
+        "moe_gated_ffn_backward", (dy_perm, r, dtype), (x, T * m * e, dtype), (w_gate, w, dtype), (w_up, w, dtype),
+        (w_down, w, dtype), (gate, hidden, dtype), (up, hidden, dtype), (offsets, 4 * (E + 1), _INDEX),
+        (perm, 4 * rows, _INDEX), (dx_perm, r, dtype), (dw_gate, w, dtype), (dw_up, w, dtype), (dw_down, w, dtype),
+        (workspace, ws_bytes, None))
+    _check("moe_gated_ffn_backward", lib().moe_gated_ffn_backward(
+        dy_perm, x, dtype, w_gate, w_up, w_down, gate, up, offsets, perm, T, topk, rows, m, p, E, dx_perm, dw_gate,
+        dw_up, dw_down, workspace, ws_bytes, _s(stream)))
+
+
+def moe_route_backward_workspace_size(T, m, E) -> int:
+    n = _sz()
+    _check("moe_route_backward_workspace_size", lib().moe_route_backward_workspace_size(T, m, E, ctypes.byref(n)))
+    return n.value
+
+
+def moe_route_backward(d_topk_w, topk_idx, topk_w, d_logits_add, x, x_dtype, w_router, dx_add, T, m, E, k, d_logits,
+                       dx=None, dw_router=None, db_router=None, workspace=None, ws_bytes=0, stream=None):
+    n = T * m * _size(x_dtype)
+    d_topk_w, topk_idx, topk_w, d_logits_add, x, w_router, dx_add, d_logits, dx, dw_router, db_router, workspace = _tensors(
+        "moe_route_backward", (d_topk_w, 4 * T * k, MOE_F32), (topk_idx, 4 * T * k, _INDEX), (topk_w, 4 * T * k, MOE_F32),
+        (d_logits_add, 4 * T * E, MOE_F32), (x, n, x_dtype), (w_router, 4 * m * E, MOE_F32), (dx_add, n, x_dtype),
+        (d_logits, 4 * T * E, MOE_F32), (dx, n, x_dtype), (dw_router, 4 * m * E, MOE_F32), (db_router, 4 * E, MOE_F32),
+        (workspace, ws_bytes, None))
+    _check("moe_route_backward", lib().moe_route_backward(d_topk_w, topk_idx, topk_w, d_logits_add, x, x_dtype, w_router,
+                                                          dx_add, T, m, E, k, d_logits, dx, dw_router, db_router,
+                                                          workspace, ws_bytes, _s(stream)))
 
 
 def moe_layer_forward(w, w_router, b_router, x, x_dtype, T, m, p, E, k, y, y_dtype, workspace, ws_bytes,

@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gemv.so")
 SOURCES = ["moe_api.cpp", "moe_route.hip", "moe_ffn_skinny.hip", "moe_ffn_gemm.hip", "moe_misc.hip", "moe_rows.hip",
-           "moe_matmul_i8.hip"]
+           "moe_matmul_i8.hip", "moe_gated.hip", "moe_gated_bf16.hip", "moe_gated_f32.hip", "moe_route_grad.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = [

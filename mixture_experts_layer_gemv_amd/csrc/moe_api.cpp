@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "moe_gemv.h"
+#include "moe_gated.hpp"
 #include "moe_index.hpp"
 #include "moe_kernels.hpp"
 #include "moe_rows.hpp"
@@ -1863,6 +1864,319 @@ moe_status moe_matmul_i8(const int8_t* x, const float* x_scale, const int8_t* w,
   a.N = N;
   a.E = E;
   MOE_TRY_HIP(run("matmul_i8", s, [&] { return moe::launch_matmul_i8(a, y_dtype == MOE_BF16, device_cus(), s); }));
+  return ok();
+}
+
+}  // extern "C"
+
+// ---- a trainable block: residual and norm, experts on plain weights, routing gradient ----
+
+namespace {
+
+moe_status check_gated(int dtype, const int32_t* offsets, const int32_t* perm, int T, int topk, int rows, int m, int p,
+                       int E) {
+  if (T < 0 || rows < 0 || m <= 0 || p <= 0 || E < 1)
+    return fail(MOE_ERR_INVALID_ARG, "bad sizes T=%d rows=%d m=%d p=%d E=%d", T, rows, m, p, E);
+  if (perm && topk < 1) return fail(MOE_ERR_INVALID_ARG, "topk=%d must be >= 1", topk);
+  if (perm && rows > 0 && T < 1) return fail(MOE_ERR_INVALID_ARG, "rows=%d of no tokens", rows);
+  if (!perm && T != rows) return fail(MOE_ERR_INVALID_ARG, "T=%d must equal rows=%d without perm", T, rows);
+  if (!offsets && E != 1) return fail(MOE_ERR_INVALID_ARG, "E=%d needs offsets", E);
+  return check_value_dtype("dtype", dtype);
+}
+
+// Sizes that the launches take: column offsets of a tile in 32 bits, fewer than
+// 2^32 threads.
+moe_status check_gated_sizes(int rows, int m, int p, int E) {
+  if (rows < 0 || m <= 0 || p <= 0 || E < 1)
+    return fail(MOE_ERR_INVALID_ARG, "bad sizes rows=%d m=%d p=%d E=%d", rows, m, p, E);
+  if (E > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "E=%d exceeds %d", E, MOE_MAX_EXPERTS);
+  if (m % 8 || p % 8) return fail(MOE_ERR_UNSUPPORTED, "m=%d and p=%d must be multiples of 8", m, p);
+  if (m > moe::kGatedMaxCols || p > moe::kGatedMaxCols)
+    return fail(MOE_ERR_UNSUPPORTED, "m=%d and p=%d may not exceed %d", m, p, moe::kGatedMaxCols);
+  const long long wide = m > p ? m : p;
+  if (((long long)rows / 64 + E) * ((wide + 127) / 128) >= 1LL << 22)
+    return fail(MOE_ERR_UNSUPPORTED, "rows=%d by %lld columns is too large", rows, wide);
+  if (3LL * E * ((m + 127) / 128) * ((p + 127) / 128) >= 1LL << 23)
+    return fail(MOE_ERR_UNSUPPORTED, "E=%d matrices of %d x %d are too large", E, m, p);
+  return MOE_OK;
+}
+
+size_t value_bytes(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
+
+// Bytes of the block's workspace: h (forward); the gradients of gate and up, h and
+// x in row order (backward).
+size_t gated_bytes(int dtype, int rows, int m, int p, bool backward) {
+  const size_t hidden = align256((size_t)rows * p * value_bytes(dtype));
+  return backward ? 3 * hidden + align256((size_t)rows * m * value_bytes(dtype)) : hidden;
+}
+
+moe_status check_workspace(const void* workspace, size_t ws_bytes, size_t need) {
+  if (!workspace || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace ? ws_bytes : (size_t)0, need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return MOE_OK;
+}
+
+bool all_aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_add_norm_forward(const void* x, const void* residual, int dtype, int norm, const float* gamma,
+                                const float* beta, float eps, int T, int m, void* sum, void* y, int8_t* codes,
+                                float* scale, float* mean, float* rstd, void* stream) {
+  if (moe_status rc = check_norm(dtype, norm, T, m)) return rc;
+  if (norm == MOE_NORM_RMS && (beta || mean)) return fail(MOE_ERR_INVALID_ARG, "the RMS norm takes no beta and no mean");
+  if (!(eps >= 0.0f) || eps > 1.0f) return fail(MOE_ERR_INVALID_ARG, "eps=%g must be in [0, 1]", (double)eps);
+  if (T == 0) return ok();
+  if (!x || !gamma || (!y && !codes)) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!codes != !scale) return fail(MOE_ERR_INVALID_ARG, "codes and scale go together");
+  if (sum && sum == y) return fail(MOE_ERR_INVALID_ARG, "sum and y must differ");
+  if (!all_aligned16({x, residual, gamma, beta, sum, y, codes}))
+    return fail(MOE_ERR_INVALID_ARG, "x, residual, gamma, beta, sum, y and codes must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  moe::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.sum = sum;
+  a.out = y;
+  a.codes = codes;
+  a.scale = scale;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.eps = eps;
+  a.T = T;
+  a.m = m;
+  MOE_TRY_HIP(run("add_norm_fwd", s, [&] {
+    return moe::launch_add_norm_forward(a, dtype == MOE_BF16, norm == MOE_NORM_LAYER, device_cus(), s);
+  }));
+  return ok();
+}
+
+moe_status moe_add_norm_backward(const void* dy, const void* dsum, const void* sum, int dtype, int norm,
+                                 const float* gamma, const float* mean, const float* rstd, int T, int m, void* dx,
+                                 float* dgamma, float* dbeta, void* workspace, size_t ws_bytes, void* stream) {
+  if (moe_status rc = check_norm(dtype, norm, T, m)) return rc;
+  if (norm == MOE_NORM_RMS && (mean || dbeta)) return fail(MOE_ERR_INVALID_ARG, "the RMS norm has no mean and no beta");
+  if (!dx && !dgamma && !dbeta) return fail(MOE_ERR_INVALID_ARG, "no output");
+  if (!all_aligned16({dx, dgamma, dbeta})) return fail(MOE_ERR_INVALID_ARG, "dx, dgamma and dbeta must be 16-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  if (T == 0) {  // the sum over no rows
+    for (float* g : {dgamma, dbeta})
+      if (g) MOE_TRY_HIP(run("fill", s, [&] { return moe::launch_fill_zero(g, (size_t)m, s); }));
+    return ok();
+  }
+  if (!dy || !sum || !gamma || !rstd || (norm == MOE_NORM_LAYER && !mean)) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!all_aligned16({dy, dsum, sum, gamma}))
+    return fail(MOE_ERR_INVALID_ARG, "dy, dsum, sum and gamma must be 16-byte aligned");
+  const bool wgrad = dgamma || dbeta;
+  if (wgrad)
+    if (moe_status rc = check_workspace(workspace, ws_bytes, norm_backward_bytes(T, m))) return rc;
+  moe::NormArgs a{};
+  a.x = sum;
+  a.dy = dy;
+  a.dsum = dsum;
+  a.gamma = gamma;
+  a.out = dx;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.partial = wgrad ? static_cast<float*>(workspace) : nullptr;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.T = T;
+  a.m = m;
+  MOE_TRY_HIP(run("add_norm_bwd", s, [&] {
+    return moe::launch_add_norm_backward(a, dtype == MOE_BF16, norm == MOE_NORM_LAYER, device_cus(), s);
+  }));
+  return ok();
+}
+
+moe_status moe_gated_ffn_workspace_size(int dtype, int rows, int m, int p, int E, int backward, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  if (moe_status rc = check_value_dtype("dtype", dtype)) return rc;
+  if (moe_status rc = check_gated_sizes(rows, m, p, E)) return rc;
+  *bytes = gated_bytes(dtype, rows, m, p, backward != 0);
+  return ok();
+}
+
+moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, const void* w_up, const void* w_down,
+                                 const int32_t* offsets, const int32_t* perm, int T, int topk, int rows, int m, int p,
+                                 int E, void* y_perm, void* gate, void* up, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  if (moe_status rc = check_gated(dtype, offsets, perm, T, topk, rows, m, p, E)) return rc;
+  if (moe_status rc = check_gated_sizes(rows, m, p, E)) return rc;
+  if (rows == 0) return ok();
+  if (!x || !w_gate || !w_up || !w_down || !y_perm) return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!gate != !up) return fail(MOE_ERR_INVALID_ARG, "gate and up go together");
+  if (!all_aligned16({x, w_gate, w_up, w_down, y_perm, gate, up}))
+    return fail(MOE_ERR_INVALID_ARG, "x, the weights, y_perm, gate and up must be 16-byte aligned");
+  if (moe_status rc = check_workspace(workspace, ws_bytes, gated_bytes(dtype, rows, m, p, false))) return rc;
+  const hipStream_t s = as_stream(stream);
+  const bool bf16 = dtype == MOE_BF16;
+  moe::GatedArgs a{};
+  a.x = x;
+  a.perm = perm;
+  a.T = T;
+  a.topk = topk;
+  a.w[0] = w_gate;
+  a.w[1] = w_up;
+  a.offsets = offsets;
+  a.R = rows;
+  a.E = E;
+  a.K = m;
+  a.N = p;
+  a.out[0] = workspace;
+  a.out[1] = gate;
+  a.out[2] = up;
+  MOE_TRY_HIP(run("gated_up", s, [&] { return moe::launch_gated_up(a, bf16, device_cus(), s); }));
+  moe::GatedArgs d{};
+  d.x = workspace;
+  d.w[0] = w_down;
+  d.offsets = offsets;
+  d.R = rows;
+  d.E = E;
+  d.K = p;
+  d.N = m;
+  d.out[0] = y_perm;
+  MOE_TRY_HIP(run("gated_down", s, [&] { return moe::launch_gated_down(d, bf16, device_cus(), s); }));
+  return ok();
+}
+
+moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype, const void* w_gate, const void* w_up,
+                                  const void* w_down, const void* gate, const void* up, const int32_t* offsets,
+                                  const int32_t* perm, int T, int topk, int rows, int m, int p, int E, void* dx_perm,
+                                  void* dw_gate, void* dw_up, void* dw_down, void* workspace, size_t ws_bytes,
+                                  void* stream) {
+  if (moe_status rc = check_gated(dtype, offsets, perm, T, topk, rows, m, p, E)) return rc;
+  if (moe_status rc = check_gated_sizes(rows, m, p, E)) return rc;
+  if (!dx_perm && !dw_gate && !dw_up && !dw_down) return fail(MOE_ERR_INVALID_ARG, "no output");
+  if (!dw_gate != !dw_up) return fail(MOE_ERR_INVALID_ARG, "dw_gate and dw_up go together");
+  if (!all_aligned16({dx_perm, dw_gate, dw_up, dw_down}))
+    return fail(MOE_ERR_INVALID_ARG, "dx_perm and the weight gradients must be 16-byte aligned");
+  const bool bf16 = dtype == MOE_BF16;
+  const size_t es = value_bytes(dtype);
+  const hipStream_t s = as_stream(stream);
+  char* dg = nullptr;
+  char* du = nullptr;
+  char* h = nullptr;
+  const void* xr = x;  // x in row order
+  if (rows > 0) {
+    if (!dy_perm || !w_gate || !w_up || !w_down || !gate || !up || (dw_gate && !x))
+      return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+    if (!all_aligned16({dy_perm, x, w_gate, w_up, w_down, gate, up}))
+      return fail(MOE_ERR_INVALID_ARG, "dy_perm, x, the weights, gate and up must be 16-byte aligned");
+    if (moe_status rc = check_workspace(workspace, ws_bytes, gated_bytes(dtype, rows, m, p, true))) return rc;
+    const size_t hidden = align256((size_t)rows * p * es);
+    dg = static_cast<char*>(workspace);
+    du = dg + hidden;
+    h = du + hidden;
+    moe::GatedArgs a{};
+    a.x = dy_perm;
+    a.w[0] = w_down;
+    a.offsets = offsets;
+    a.R = rows;
+    a.E = E;
+    a.K = m;
+    a.N = p;
+    a.in[0] = gate;
+    a.in[1] = up;
+    a.out[0] = dg;
+    a.out[1] = du;
+    a.out[2] = dw_down ? h : nullptr;
+    MOE_TRY_HIP(run("gated_grad_hidden", s, [&] { return moe::launch_gated_grad_hidden(a, bf16, device_cus(), s); }));
+    if (dw_gate && perm) {
+      char* const rows_x = h + hidden;
+      MOE_TRY_HIP(run("gather_rows", s, [&] {
+        return moe::launch_gather_rows(x, perm, T, topk, rows, (long long)m * es, rows_x, s);
+      }));
+      xr = rows_x;
+    }
+  }
+  if (dw_gate || dw_down) {
+    moe::GradWArgs w{};
+    w.offsets = offsets;
+    w.R = rows;
+    w.E = E;
+    if (dw_gate) {
+      w.p[w.n++] = {xr, dg, dw_gate, m, p};
+      w.p[w.n++] = {xr, du, dw_up, m, p};
+    }
+    if (dw_down) w.p[w.n++] = {h, dy_perm, dw_down, p, m};
+    MOE_TRY_HIP(run("gated_grad_w", s, [&] { return moe::launch_gated_grad_w(w, bf16, device_cus(), s); }));
+  }
+  if (dx_perm && rows > 0) {
+    moe::GatedArgs a{};
+    a.x = dg;
+    a.x2 = du;
+    a.w[0] = w_gate;
+    a.w[1] = w_up;
+    a.offsets = offsets;
+    a.R = rows;
+    a.E = E;
+    a.K = p;
+    a.N = m;
+    a.out[0] = dx_perm;
+    MOE_TRY_HIP(run("gated_grad_x", s, [&] { return moe::launch_gated_grad_x(a, bf16, device_cus(), s); }));
+  }
+  return ok();
+}
+
+moe_status moe_route_backward_workspace_size(int T, int m, int E, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  if (moe_status rc = check_rows_shape(T, m)) return rc;
+  if (E < 1) return fail(MOE_ERR_INVALID_ARG, "E=%d must be >= 1", E);
+  if (E > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "E=%d exceeds %d", E, MOE_MAX_EXPERTS);
+  *bytes = T > 0 ? moe::route_grad_bytes(T, m, E, device_cus()) : 0;
+  return ok();
+}
+
+moe_status moe_route_backward(const float* d_topk_w, const int32_t* topk_idx, const float* topk_w,
+                              const float* d_logits_add, const void* x, int x_dtype, const float* w_router,
+                              const void* dx_add, int T, int m, int E, int k, float* d_logits, void* dx,
+                              float* dw_router, float* db_router, void* workspace, size_t ws_bytes, void* stream) {
+  if (moe_status rc = check_assignments(T, m, k, 0)) return rc;
+  if (E < 1 || k > E) return fail(MOE_ERR_INVALID_ARG, "k=%d must be in [1, E=%d]", k, E);
+  if (E > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "E=%d exceeds %d", E, MOE_MAX_EXPERTS);
+  if (moe_status rc = check_value_dtype("x dtype", x_dtype)) return rc;
+  if (m > moe::kGatedMaxCols) return fail(MOE_ERR_UNSUPPORTED, "m=%d exceeds %d", m, moe::kGatedMaxCols);
+  const hipStream_t s = as_stream(stream);
+  if (T == 0) {  // the sums over no tokens
+    if (dw_router) MOE_TRY_HIP(run("fill", s, [&] { return moe::launch_fill_zero(dw_router, (size_t)m * E, s); }));
+    if (db_router) MOE_TRY_HIP(run("fill", s, [&] { return moe::launch_fill_zero(db_router, (size_t)E, s); }));
+    return ok();
+  }
+  const bool wgrad = dw_router || db_router;
+  if (!d_topk_w || !topk_idx || !topk_w || !d_logits || (dw_router && !x) || (dx && !w_router))
+    return fail(MOE_ERR_INVALID_ARG, "NULL argument");
+  if (!all_aligned16({x, dx_add, dx})) return fail(MOE_ERR_INVALID_ARG, "x, dx_add and dx must be 16-byte aligned");
+  if (wgrad)
+    if (moe_status rc = check_workspace(workspace, ws_bytes, moe::route_grad_bytes(T, m, E, device_cus()))) return rc;
+  moe::RouteGradArgs a{};
+  a.dw = d_topk_w;
+  a.idx = topk_idx;
+  a.w = topk_w;
+  a.dl_add = d_logits_add;
+  a.x = x;
+  a.wr = w_router;
+  a.dx_add = dx_add;
+  a.dl = d_logits;
+  a.dx = dx;
+  a.dwr = dw_router;
+  a.db = db_router;
+  a.partial = static_cast<float*>(workspace);
+  a.T = T;
+  a.m = m;
+  a.E = E;
+  a.k = k;
+  MOE_TRY_HIP(run("route_bwd", s, [&] { return moe::launch_route_backward(a, x_dtype == MOE_BF16, device_cus(), s); }));
   return ok();
 }
 

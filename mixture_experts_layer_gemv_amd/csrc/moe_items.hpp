@@ -1,0 +1,76 @@
+// The work items of a launch over the experts' rows, found on the device from a
+// dispatch's offsets; shared by the int8 product and the gated feed-forward
+// block.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe_index.hpp"
+
+namespace moe {
+
+// One (expert, row block, column block) of a launch.
+struct Item {
+  int e, mb, nb;   // e < 0: none
+  int blocks;      // row blocks of the expert
+  int row0, rows;  // the block's first row and its rows
+};
+
+// Item L of the launch's work order (see gemm_item; cg = 0: row blocks
+// outermost), found by every wave for itself: each lane holds an expert.  The
+// offsets are clamped to [0, R], a decreasing entry counting as its
+// predecessor, so that the ranges are disjoint and in bounds whatever the
+// caller's array holds.  spread: L is the block's number, dealt evenly over
+// the XCDs (xcd_item); else it is the item.
+__device__ __forceinline__ Item find_item(const int32_t* offsets, int E, int R, int BM, int NBL, int cg, int L, bool spread) {
+  Item it{-1, 0, 0, 0, 0, 0};
+  int e = 0, lo = 0, hi = R, before = 0;  // the item's expert, its rows, the items before it
+  if (!offsets) {
+    const int total = (hi + BM - 1) / BM * NBL;
+    if (spread) L = xcd_item(L, total, 0);
+    if (L < 0 || L >= total) return it;
+  } else {
+    const int lane = threadIdx.x & 63;
+    auto clamped = [&](int i) { return min(max(i <= E ? offsets[i] : 0, 0), R); };
+    int first = clamped(lane);
+    const int next = clamped(lane + 1);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int p = __shfl_up(first, d, 64);
+      if (lane >= d) first = max(first, p);
+    }
+    const int end = max(first, next);
+    const int items = lane < E ? (end - first + BM - 1) / BM * NBL : 0;
+    int sum = items;  // of the experts up to this one
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int p = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += p;
+    }
+    const int total = __builtin_amdgcn_readlane(sum, 63);
+    if (spread) L = xcd_item(L, total, 0);
+    if (L < 0 || L >= total) return it;
+    e = __builtin_ctzll(__ballot(L < sum));
+    before = __builtin_amdgcn_readlane(sum - items, e);
+    lo = __builtin_amdgcn_readlane(first, e);
+    hi = __builtin_amdgcn_readlane(end, e);
+  }
+  const int blocks = (hi - lo + BM - 1) / BM, li = L - before;
+  if (cg) {
+    const int g = li / (blocks * cg), rem = li - g * blocks * cg;
+    const int gw = min(NBL - g * cg, cg);
+    it.mb = rem / gw;
+    it.nb = g * cg + (rem - it.mb * gw);
+  } else {
+    it.mb = li / NBL;
+    it.nb = li - it.mb * NBL;
+  }
+  it.e = e;
+  it.blocks = blocks;
+  it.row0 = lo + it.mb * BM;
+  it.rows = min(BM, hi - it.row0);
+  return it;
+}
+
+}  // namespace moe

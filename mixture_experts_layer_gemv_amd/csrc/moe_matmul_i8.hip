@@ -11,6 +11,7 @@
 // token.
 #include <type_traits>
 
+#include "moe_items.hpp"
 #include "moe_kernels.hpp"
 #include "moe_lds.hpp"
 #include "moe_rows.hpp"
@@ -23,69 +24,6 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
-// One (expert, row block, column block) of a launch.
-struct Item {
-  int e, mb, nb;   // e < 0: none
-  int blocks;      // row blocks of the expert
-  int row0, rows;  // the block's first row and its rows
-};
-
-// Item L of the launch's work order (see gemm_item; cg = 0: row blocks
-// outermost), found by every wave for itself: each lane holds an expert.  The
-// offsets are clamped to [0, R], a decreasing entry counting as its
-// predecessor, so that the ranges are disjoint and in bounds whatever the
-// caller's array holds.  spread: L is the block's number, dealt evenly over
-// the XCDs (xcd_item); else it is the item.
-__device__ __forceinline__ Item find_item(const I8Args& A, int BM, int NBL, int cg, int L, bool spread) {
-  Item it{-1, 0, 0, 0, 0, 0};
-  int e = 0, lo = 0, hi = A.R, before = 0;  // the item's expert, its rows, the items before it
-  if (!A.offsets) {
-    const int total = (hi + BM - 1) / BM * NBL;
-    if (spread) L = xcd_item(L, total, 0);
-    if (L < 0 || L >= total) return it;
-  } else {
-    const int lane = threadIdx.x & 63;
-    auto clamped = [&](int i) { return min(max(i <= A.E ? A.offsets[i] : 0, 0), A.R); };
-    int first = clamped(lane);
-    const int next = clamped(lane + 1);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int p = __shfl_up(first, d, 64);
-      if (lane >= d) first = max(first, p);
-    }
-    const int end = max(first, next);
-    const int items = lane < A.E ? (end - first + BM - 1) / BM * NBL : 0;
-    int sum = items;  // of the experts up to this one
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int p = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += p;
-    }
-    const int total = __builtin_amdgcn_readlane(sum, 63);
-    if (spread) L = xcd_item(L, total, 0);
-    if (L < 0 || L >= total) return it;
-    e = __builtin_ctzll(__ballot(L < sum));
-    before = __builtin_amdgcn_readlane(sum - items, e);
-    lo = __builtin_amdgcn_readlane(first, e);
-    hi = __builtin_amdgcn_readlane(end, e);
-  }
-  const int blocks = (hi - lo + BM - 1) / BM, li = L - before;
-  if (cg) {
-    const int g = li / (blocks * cg), rem = li - g * blocks * cg;
-    const int gw = min(NBL - g * cg, cg);
-    it.mb = rem / gw;
-    it.nb = g * cg + (rem - it.mb * gw);
-  } else {
-    it.mb = li / NBL;
-    it.nb = li - it.mb * NBL;
-  }
-  it.e = e;
-  it.blocks = blocks;
-  it.row0 = lo + it.mb * BM;
-  it.rows = min(BM, hi - it.row0);
-  return it;
-}
 
 // The x row of output row r, kept inside [0, T).
 __device__ __forceinline__ int token_of(const I8Args& A, int r) {
@@ -162,7 +100,7 @@ __global__ __launch_bounds__(W * 64) void k_i8_rows(const I8Args A, int cols) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[RING > PART ? RING : PART];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // row blocks outermost: neighbouring workgroups, on different XCDs, read neighbouring channels
-  const Item it = find_item(A, 16 * TB, cols, 0, (int)blockIdx.x, false);
+  const Item it = find_item(A.offsets, A.E, A.R, 16 * TB, cols, 0, (int)blockIdx.x, false);
   if (it.e < 0) return;
   const int e = it.e, n0 = it.nb * 16 * CB, row0 = it.row0, rows = it.rows;
 
@@ -300,7 +238,7 @@ void k_i8_tile(const I8Args A, int cg, bool rotate) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WC, wc = wave % WC;
-  const Item it = find_item(A, Sh::BM, (A.N + Sh::BN - 1) / Sh::BN, cg, (int)blockIdx.x, true);
+  const Item it = find_item(A.offsets, A.E, A.R, Sh::BM, (A.N + Sh::BN - 1) / Sh::BN, cg, (int)blockIdx.x, true);
   if (it.e < 0) return;
   const int e = it.e, row0 = it.row0, rows = it.rows, n0 = it.nb * Sh::BN;
 

@@ -11,6 +11,7 @@
 // combine's gradient 66.4 us (5.1).
 #include <type_traits>
 
+#include "moe_convert.hpp"
 #include "moe_kernels.hpp"
 #include "moe_rows.hpp"
 #include "moe_rows_index.hpp"
@@ -154,12 +155,30 @@ __device__ __forceinline__ float team_sum(float v, int NT, int first, float* slo
   return group_sum((lane & 15) < waves ? slot[first + (lane & 15)] : 0.0f, 16);
 }
 
+// The largest value of a team, as team_sum.
+__device__ __forceinline__ float team_max(float v, int NT, int first, float* slot) {
+  for (int o = 1; o < (NT < 64 ? NT : 64); o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  if (NT <= 64) return v;
+  const int lane = threadIdx.x & 63, waves = NT >> 6;
+  if (lane == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = (lane & 15) < waves ? slot[first + (lane & 15)] : 0.0f;
+  for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
 // y = (x - mu) r gamma + beta, mu the row's mean (0 for the RMS norm), r = 1 /
 // sqrt(mean((x - mu)^2) + eps).  gamma and beta stay in registers from row to
 // row; the next row is loaded while this one is summed.
-template <bool BF16, int V, bool LAYER, bool ONCE>
+//
+// ADD: x + residual in place of x, kept in fp32 for the norm and rounded once to
+// be stored as sum; y may be absent, and its int8 codes with the row's power-of-two
+// scale (act_scale_exponent) are taken from the fp32 values, not from rounded
+// ones.  sum and y may lie over x or residual: a row is read whole by the team
+// that writes it, before it does.
+template <bool BF16, int V, bool LAYER, bool ONCE, bool ADD>
 __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
-  __shared__ float red[2][16];
+  __shared__ float red[3][16];
   const int team = threadIdx.x / NT, teams = blockDim.x / NT, tid = threadIdx.x - team * NT;
   const int first = team * NT >> 6;  // the team's first wave
   const int m = A.m;
@@ -174,11 +193,15 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
   }
-  u32x4_t next[V][BF16 ? 1 : 2];
+  u32x4_t next[V][BF16 ? 1 : 2], nres[ADD ? V : 1][BF16 ? 1 : 2];
   auto fetch = [&](long long t) {
     if (t >= A.T) t = A.T - 1;  // read, never written
 #pragma unroll
-    for (int v = 0; v < V; ++v) load_raw<BF16, ONCE>(next[v], A.x, (size_t)t * m, norm_cols(BF16, tid, NT, v), m);
+    for (int v = 0; v < V; ++v) {
+      load_raw<BF16, ONCE>(next[v], A.x, (size_t)t * m, norm_cols(BF16, tid, NT, v), m);
+      if (ADD && A.residual)
+        load_raw<BF16, ONCE>(nres[v], A.residual, (size_t)t * m, norm_cols(BF16, tid, NT, v), m);
+    }
   };
   const long long stride = (long long)gridDim.x * teams;
   fetch((long long)blockIdx.x * teams + team);
@@ -187,8 +210,20 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
     const long long t = t0 + team;
     float f[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) from_raw<BF16>(next[v], f[v]);
+    for (int v = 0; v < V; ++v) {
+      from_raw<BF16>(next[v], f[v]);
+      if (ADD && A.residual) {
+        float r[8];
+        from_raw<BF16>(nres[v], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[v][j] += r[j];
+      }
+    }
     if (t0 + stride < A.T) fetch(t + stride);
+    if constexpr (ADD)
+      if (A.sum && t < A.T)
+#pragma unroll
+        for (int v = 0; v < V; ++v) store_row<BF16>(A.sum, (size_t)t * m, norm_cols(BF16, tid, NT, v), m, f[v]);
     float mu = 0.0f;
     if constexpr (LAYER) {
       float s = 0.0f;
@@ -211,17 +246,54 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
     }
     const float var = team_sum(q, NT, first, red[LAYER ? 1 : turn]) * inv_m;
     const float r = 1.0f / sqrtf(var + A.eps);
-    if (t >= A.T) continue;
-    if (tid == 0) {
+    if (tid == 0 && t < A.T) {
       if (LAYER && A.mean) A.mean[t] = mu;
       if (A.rstd) A.rstd[t] = r;
     }
+    if constexpr (!ADD) {
+      if (t >= A.T) continue;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float o[8];
+      for (int v = 0; v < V; ++v) {
+        float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = LAYER ? fmaf(f[v][j] * r, g[v][j], b[v][j]) : f[v][j] * r * g[v][j];
-      store_row<BF16>(A.out, (size_t)t * m, norm_cols(BF16, tid, NT, v), m, o);
+        for (int j = 0; j < 8; ++j) o[j] = LAYER ? fmaf(f[v][j] * r, g[v][j], b[v][j]) : f[v][j] * r * g[v][j];
+        store_row<BF16>(A.out, (size_t)t * m, norm_cols(BF16, tid, NT, v), m, o);
+      }
+    } else {
+      float top = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)  // past the row's end gamma and beta are 0, and so is y
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[v][j] = LAYER ? fmaf(f[v][j] * r, g[v][j], b[v][j]) : f[v][j] * r * g[v][j];
+          top = fmaxf(top, fabsf(f[v][j]));
+        }
+      if (A.out && t < A.T)
+#pragma unroll
+        for (int v = 0; v < V; ++v) store_row<BF16>(A.out, (size_t)t * m, norm_cols(BF16, tid, NT, v), m, f[v]);
+      if (!A.codes) continue;
+      const int X = act_scale_exponent<true>(team_max(top, NT, first, red[2]));
+      if (t >= A.T) continue;
+      if (tid == 0) A.scale[t] = ldexpf(1.0f, X);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const NormCols c = norm_cols(BF16, tid, NT, v);
+        uint32_t q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          q[h] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            q[h] |= ((uint32_t)(int)rintf(ldexpf(f[v][4 * h + j], -X)) & 0xFFu) << (8 * j);
+        }
+        int8_t* const row = A.codes + (size_t)t * m;
+        if constexpr (BF16) {
+          if (c.lo < m) *reinterpret_cast<u32x2_t*>(row + c.lo) = u32x2_t{q[0], q[1]};
+        } else {
+          if (c.lo < m) *reinterpret_cast<uint32_t*>(row + c.lo) = q[0];
+          if (c.hi < m) *reinterpret_cast<uint32_t*>(row + c.hi) = q[1];
+        }
+      }
     }
   }
 }
@@ -232,7 +304,9 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
 // A thread adds its columns' dy h and dy over the rows its team takes.  The
 // block's sums are added in LDS and written as one row of partial sums, and
 // k_norm_wgrad adds those in block order: nothing depends on timing.
-template <bool BF16, int V, bool LAYER, bool ONCE>
+// ADD: dsum, the gradient that reaches the sum of x and residual directly, is
+// added to dx, which may lie over dsum or dy as the forward's rows may.
+template <bool BF16, int V, bool LAYER, bool ONCE, bool ADD>
 __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
   __shared__ float red[4][16];
   extern __shared__ float acc[];  // [2][m] where the block's sums are added
@@ -247,7 +321,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) ag[v][j] = ab[v][j] = 0.0f;
   }
-  u32x4_t nx[V][BF16 ? 1 : 2], ny[V][BF16 ? 1 : 2];
+  u32x4_t nx[V][BF16 ? 1 : 2], ny[V][BF16 ? 1 : 2], ns[ADD ? V : 1][BF16 ? 1 : 2];
   float nmu = 0.0f, nr = 0.0f;
   auto fetch = [&](long long t) {
     const long long row = t < A.T ? t : A.T - 1;
@@ -256,6 +330,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
       const NormCols c = norm_cols(BF16, tid, NT, v);
       load_raw<BF16, ONCE>(nx[v], A.x, (size_t)row * m, c, m);
       load_raw<BF16, ONCE>(ny[v], A.dy, (size_t)row * m, c, m);
+      if (ADD && A.dsum) load_raw<BF16, ONCE>(ns[v], A.dsum, (size_t)row * m, c, m);
     }
     nmu = LAYER ? A.mean[row] : 0.0f;
     nr = A.rstd[row];
@@ -274,11 +349,15 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
     if (!AHEAD) fetch(t);
     const float mu = nmu, r = nr;
     float h[V][8], u[V][8];
+    u32x4_t ds[ADD ? V : 1][BF16 ? 1 : 2];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       from_raw<BF16>(nx[v], h[v]);
       from_raw<BF16>(ny[v], u[v]);
+      if constexpr (ADD)
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) ds[v][i] = ns[v][i];
     }
     if (AHEAD && t0 + stride < A.T) fetch(t + stride);
 #pragma unroll
@@ -327,6 +406,13 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(const NormArgs A, int NT) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (LAYER ? u[v][j] - m2 - h[v][j] * m1 : u[v][j] - h[v][j] * m1) * r;
+      if constexpr (ADD)
+        if (A.dsum) {
+          float d[8];
+          from_raw<BF16>(ds[v], d);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] += d[j];
+        }
       store_row<BF16>(A.out, (size_t)t * m, norm_cols(BF16, tid, NT, v), m, o);
     }
   }
@@ -616,7 +702,10 @@ long long bytes_of(long long rows, int m, bool bf16) { return rows * m * (bf16 ?
 
 }  // namespace
 
-hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
+namespace {
+
+template <bool ADD>
+hipError_t norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, long long bytes, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
   const int V = norm_vecs(a.m), nt = norm_threads(a.m), teams = norm_fwd_teams(nt), threads = nt * teams;
@@ -625,14 +714,15 @@ hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus
   dispatch(
       [&](auto b, auto l, auto big) {
         constexpr bool B = decltype(b)::value, L = decltype(l)::value, ONCE = decltype(big)::value;
-        if (V == 1) k_norm_fwd<B, 1, L, ONCE><<<grid, threads, 0, s>>>(a, nt);
-        else k_norm_fwd<B, 2, L, ONCE><<<grid, threads, 0, s>>>(a, nt);
+        if (V == 1) k_norm_fwd<B, 1, L, ONCE, ADD><<<grid, threads, 0, s>>>(a, nt);
+        else k_norm_fwd<B, 2, L, ONCE, ADD><<<grid, threads, 0, s>>>(a, nt);
       },
-      bf16, layer, large(2 * bytes_of(a.T, a.m, bf16)));
+      bf16, layer, large(bytes));
   return hipGetLastError();
 }
 
-hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
+template <bool ADD>
+hipError_t norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, long long bytes, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   if (a.m <= 0 || a.m % 8 || a.m > kNormMaxCols) return hipErrorInvalidValue;
   const int V = norm_vecs(a.m), nt = norm_threads(a.m), threads = nt * norm_bwd_teams(nt);
@@ -641,14 +731,33 @@ hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cu
   dispatch(
       [&](auto b, auto l, auto big) {
         constexpr bool B = decltype(b)::value, L = decltype(l)::value, ONCE = decltype(big)::value;
-        if (V == 1) k_norm_bwd<B, 1, L, ONCE><<<grid, threads, lds, s>>>(a, nt);
-        else k_norm_bwd<B, 2, L, ONCE><<<grid, threads, lds, s>>>(a, nt);
+        if (V == 1) k_norm_bwd<B, 1, L, ONCE, ADD><<<grid, threads, lds, s>>>(a, nt);
+        else k_norm_bwd<B, 2, L, ONCE, ADD><<<grid, threads, lds, s>>>(a, nt);
       },
-      bf16, layer, large((a.out ? 3 : 2) * bytes_of(a.T, a.m, bf16)));
+      bf16, layer, large(bytes));
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !a.partial || grid == 1) return e;
   k_norm_wgrad<<<dim3((unsigned)((a.m + 31) / 32), layer ? 2 : 1), 512, 0, s>>>(a.partial, (int)grid, a.m, a.dgamma,
                                                                                layer ? a.dbeta : nullptr);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
+  return norm_forward<false>(a, bf16, layer, cus, 2 * bytes_of(a.T, a.m, bf16), s);
+}
+
+hipError_t launch_add_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
+  const int passes = 1 + (a.residual ? 1 : 0) + (a.sum ? 1 : 0) + (a.out ? 1 : 0);
+  return norm_forward<true>(a, bf16, layer, cus, passes * bytes_of(a.T, a.m, bf16) + (a.codes ? (long long)a.T * a.m : 0), s);
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
+  return norm_backward<false>(a, bf16, layer, cus, (a.out ? 3 : 2) * bytes_of(a.T, a.m, bf16), s);
+}
+
+hipError_t launch_add_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s) {
+  return norm_backward<true>(a, bf16, layer, cus, (a.out ? (a.dsum ? 4 : 3) : 2) * bytes_of(a.T, a.m, bf16), s);
 }
 
 hipError_t launch_permute_rows(const RowsArgs& a, bool bf16, hipStream_t s) {

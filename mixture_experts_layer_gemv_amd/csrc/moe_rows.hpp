@@ -24,9 +24,17 @@ struct NormArgs {
   float* dbeta;        // [m] or null
   float eps;
   int T, m;
+  // with the residual's addition (add_norm):
+  const void* residual;  // forward: [T][m] or null
+  void* sum;             // forward: x + residual [T][m], or null
+  int8_t* codes;         // forward: [T][m] or null
+  float* scale;          // forward, with codes: [T]
+  const void* dsum;      // backward: [T][m], added to dx, or null
 };
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s);
+hipError_t launch_add_norm_forward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s);
+hipError_t launch_add_norm_backward(const NormArgs& a, bool bf16, bool layer, int cus, hipStream_t s);
 
 struct RowsArgs {
   const void* tok;     // token rows [T][m]: x (permute), dy (combine's gradient)
