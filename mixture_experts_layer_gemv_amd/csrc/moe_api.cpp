@@ -1903,14 +1903,28 @@ moe_status check_gated_sizes(int rows, int m, int p, int E) {
 
 size_t value_bytes(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
-// Bytes of the block's workspace: h (forward); the gradients of gate and up, h and
-// x in row order (backward).
-size_t gated_bytes(int dtype, int rows, int m, int p, bool backward) {
-  const size_t hidden = align256((size_t)rows * p * value_bytes(dtype));
-  return backward ? 3 * hidden + align256((size_t)rows * m * value_bytes(dtype)) : hidden;
+// The block's workspace: the rows that one product hands to the next (forward: h;
+// backward: the gradients of gate and up, h, and x in row order), then the partial
+// sums of a split reduction, which the products use in turn.
+struct GatedSpace {
+  size_t hidden, rows, part;
+  size_t bytes(bool backward) const { return backward ? 3 * hidden + rows + part : hidden + part; }
+};
+GatedSpace gated_space(int dtype, int rows, int m, int p, int E, bool backward) {
+  const size_t es = value_bytes(dtype);
+  const bool bf16 = dtype == MOE_BF16;
+  const int cus = device_cus();
+  GatedSpace s;
+  s.hidden = align256((size_t)rows * p * es);
+  s.rows = align256((size_t)rows * m * es);
+  s.part = backward ? std::max(moe::gated_part_bytes(bf16, false, rows, m, p, E, 1, cus),
+                               moe::gated_part_bytes(bf16, false, rows, p, m, E, 2, cus))
+                    : std::max(moe::gated_part_bytes(bf16, true, rows, m, p, E, 1, cus),
+                               moe::gated_part_bytes(bf16, false, rows, p, m, E, 1, cus));
+  return s;
 }
 
-moe_status check_workspace(const void* workspace, size_t ws_bytes, size_t need) {
+moe_status check_space(const void* workspace, size_t ws_bytes, size_t need) {
   if (!workspace || ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace ? ws_bytes : (size_t)0, need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -1979,7 +1993,7 @@ moe_status moe_add_norm_backward(const void* dy, const void* dsum, const void* s
     return fail(MOE_ERR_INVALID_ARG, "dy, dsum, sum and gamma must be 16-byte aligned");
   const bool wgrad = dgamma || dbeta;
   if (wgrad)
-    if (moe_status rc = check_workspace(workspace, ws_bytes, norm_backward_bytes(T, m))) return rc;
+    if (moe_status rc = check_space(workspace, ws_bytes, norm_backward_bytes(T, m))) return rc;
   moe::NormArgs a{};
   a.x = sum;
   a.dy = dy;
@@ -2003,7 +2017,7 @@ moe_status moe_gated_ffn_workspace_size(int dtype, int rows, int m, int p, int E
   if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
   if (moe_status rc = check_value_dtype("dtype", dtype)) return rc;
   if (moe_status rc = check_gated_sizes(rows, m, p, E)) return rc;
-  *bytes = gated_bytes(dtype, rows, m, p, backward != 0);
+  *bytes = gated_space(dtype, rows, m, p, E, backward != 0).bytes(backward != 0);
   return ok();
 }
 
@@ -2018,7 +2032,9 @@ moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, c
   if (!gate != !up) return fail(MOE_ERR_INVALID_ARG, "gate and up go together");
   if (!all_aligned16({x, w_gate, w_up, w_down, y_perm, gate, up}))
     return fail(MOE_ERR_INVALID_ARG, "x, the weights, y_perm, gate and up must be 16-byte aligned");
-  if (moe_status rc = check_workspace(workspace, ws_bytes, gated_bytes(dtype, rows, m, p, false))) return rc;
+  const GatedSpace space = gated_space(dtype, rows, m, p, E, false);
+  if (moe_status rc = check_space(workspace, ws_bytes, space.bytes(false))) return rc;
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + space.hidden);
   const hipStream_t s = as_stream(stream);
   const bool bf16 = dtype == MOE_BF16;
   moe::GatedArgs a{};
@@ -2034,6 +2050,7 @@ moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, c
   a.K = m;
   a.N = p;
   a.out[0] = workspace;
+  a.part = part;
   a.out[1] = gate;
   a.out[2] = up;
   MOE_TRY_HIP(run("gated_up", s, [&] { return moe::launch_gated_up(a, bf16, device_cus(), s); }));
@@ -2046,6 +2063,7 @@ moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, c
   d.K = p;
   d.N = m;
   d.out[0] = y_perm;
+  d.part = part;
   MOE_TRY_HIP(run("gated_down", s, [&] { return moe::launch_gated_down(d, bf16, device_cus(), s); }));
   return ok();
 }
@@ -2067,17 +2085,19 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
   char* dg = nullptr;
   char* du = nullptr;
   char* h = nullptr;
+  float* part = nullptr;
   const void* xr = x;  // x in row order
   if (rows > 0) {
     if (!dy_perm || !w_gate || !w_up || !w_down || !gate || !up || (dw_gate && !x))
       return fail(MOE_ERR_INVALID_ARG, "NULL argument");
     if (!all_aligned16({dy_perm, x, w_gate, w_up, w_down, gate, up}))
       return fail(MOE_ERR_INVALID_ARG, "dy_perm, x, the weights, gate and up must be 16-byte aligned");
-    if (moe_status rc = check_workspace(workspace, ws_bytes, gated_bytes(dtype, rows, m, p, true))) return rc;
-    const size_t hidden = align256((size_t)rows * p * es);
+    const GatedSpace space = gated_space(dtype, rows, m, p, E, true);
+    if (moe_status rc = check_space(workspace, ws_bytes, space.bytes(true))) return rc;
     dg = static_cast<char*>(workspace);
-    du = dg + hidden;
-    h = du + hidden;
+    du = dg + space.hidden;
+    h = du + space.hidden;
+    part = reinterpret_cast<float*>(h + space.hidden + space.rows);
     moe::GatedArgs a{};
     a.x = dy_perm;
     a.w[0] = w_down;
@@ -2091,9 +2111,10 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
     a.out[0] = dg;
     a.out[1] = du;
     a.out[2] = dw_down ? h : nullptr;
+    a.part = part;
     MOE_TRY_HIP(run("gated_grad_hidden", s, [&] { return moe::launch_gated_grad_hidden(a, bf16, device_cus(), s); }));
     if (dw_gate && perm) {
-      char* const rows_x = h + hidden;
+      char* const rows_x = h + space.hidden;
       MOE_TRY_HIP(run("gather_rows", s, [&] {
         return moe::launch_gather_rows(x, perm, T, topk, rows, (long long)m * es, rows_x, s);
       }));
@@ -2124,6 +2145,7 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
     a.K = p;
     a.N = m;
     a.out[0] = dx_perm;
+    a.part = part;
     MOE_TRY_HIP(run("gated_grad_x", s, [&] { return moe::launch_gated_grad_x(a, bf16, device_cus(), s); }));
   }
   return ok();
@@ -2158,7 +2180,7 @@ moe_status moe_route_backward(const float* d_topk_w, const int32_t* topk_idx, co
     return fail(MOE_ERR_INVALID_ARG, "NULL argument");
   if (!all_aligned16({x, dx_add, dx})) return fail(MOE_ERR_INVALID_ARG, "x, dx_add and dx must be 16-byte aligned");
   if (wgrad)
-    if (moe_status rc = check_workspace(workspace, ws_bytes, moe::route_grad_bytes(T, m, E, device_cus()))) return rc;
+    if (moe_status rc = check_space(workspace, ws_bytes, moe::route_grad_bytes(T, m, E, device_cus()))) return rc;
   moe::RouteGradArgs a{};
   a.dw = d_topk_w;
   a.idx = topk_idx;

@@ -2,6 +2,8 @@
 // the experts' order for a weight gradient, whose reduction runs over them.
 #include "moe_gated.hpp"
 
+#include "moe_gated_index.hpp"
+
 namespace moe {
 namespace {
 
@@ -30,6 +32,14 @@ hipError_t launch_gather_rows(const void* x, const int32_t* perm, int T, int top
   k_gather_rows<<<(unsigned)(blocks < 1 << 22 ? blocks : 1 << 22), 256, 0, s>>>(
       static_cast<const u32x4_t*>(x), perm, T, topk, R, bytes / 16, static_cast<u32x4_t*>(out));
   return hipGetLastError();
+}
+
+size_t gated_part_bytes(bool bf16, bool gated, int R, int K, int N, int E, int terms, int cus) {
+  if (R <= 0) return 0;
+  const long long lines = gated ? 2LL * N : N;
+  const int steps = stage_steps(bf16 ? 2 : 4);
+  const GatedChoice c = choose_gated(bf16, R, lines, (K + steps - 1) / steps * terms, E, cus);
+  return c.splits > 1 ? (size_t)c.splits * R * lines * sizeof(float) : 0;
 }
 
 hipError_t gated_up_bf16(const GatedArgs& a, int cus, hipStream_t s);

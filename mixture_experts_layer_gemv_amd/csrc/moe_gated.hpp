@@ -24,7 +24,10 @@ struct GatedArgs {
   int R, E, K, N;          // rows, experts, reduction, output columns
   void* out[3];
   const void* in[2];       // gate, up [R][N] (gradient of the hidden rows)
+  float* part;             // workspace of a split reduction (gated_part_bytes), or null: none is split
 };
+// Bytes of `part` for a product of R rows with N output columns, by a reduction of K.
+size_t gated_part_bytes(bool bf16, bool gated, int R, int K, int N, int E, int terms, int cus);
 
 // The products with a weight gradient: out [E][M][N] = sum over an expert's
 // rows r of x[r][i] w[r][j].

@@ -45,6 +45,21 @@ MOE_HD inline int step_read_f32(int lane, int ks, int i) {
   return k * 128 + 16 * step_place(k, (lane & 31) >> 2) + 4 * (lane & 3);
 }
 
+// Block b's expert and tile (of `tiles` of every expert) in a launch of 8
+// ceil(tiles / 8) E blocks; e >= E: none.  Every XCD (b % 8) takes an eighth of each
+// expert's tiles, one expert after the other: the experts' reductions differ in
+// length, so an XCD that took whole experts would end before the others (16 experts
+// of 410 to 1640 rows, three gradients of 4096 x 6400: 4.24 ms, so 2.43).
+struct ExpertItem {
+  int e, tile;
+};
+MOE_HD inline ExpertItem expert_item(int b, int tiles) {
+  const int x = b & 7, j = b >> 3;
+  const int lo = (int)((long long)x * tiles / 8), mine = (int)((long long)(x + 1) * tiles / 8) - lo;
+  if (!mine) return {1 << 30, 0};
+  return {j / mine, lo + j % mine};
+}
+
 // The 32-channel block of a tile's W lines that a wave's block c is.  Gated tiles
 // hold their gate channels in the first half of the lines and the same channels
 // of up in the second, and a wave takes both of each: c < CB / 2 is gate.
@@ -52,6 +67,68 @@ MOE_HD inline int channel_block(bool gated, int WC, int CB, int wc, int c) {
   if (!gated) return wc * CB + c;
   const int h = CB / 2;
   return c < h ? wc * h + c : WC * h + wc * h + (c - h);
+}
+
+// The tiles of the products over the experts' rows, by rows x weight lines x stages
+// (a gated tile's lines are half gate, half up).
+enum GatedTile {
+  kGated256x256x2,
+  kGated128x256x3,
+  kGated128x128x2,
+  kGated64x128x3,
+  kGated32x256x2,
+  kGated32x256x3,
+  kGated32x128x2,
+  kGatedTiles
+};
+
+// A product's tile; the number of blocks that share a tile's reduction, each of them
+// some of its stages (their partial sums are joined by a second launch); and
+// whether the weights are read as not to be kept in the caches.
+struct GatedChoice {
+  GatedTile tile;
+  int splits;
+  bool once;
+};
+
+// The choice for R >= 1 rows of E experts, `lines` weight lines (output columns,
+// twice that for gate and up) and `stages` stages of all terms on `cus` CUs.
+inline GatedChoice choose_gated(bool bf16, int R, long long lines, int stages, int E, int cus) {
+  const long long experts = R < E ? R : E, avg = (R + experts - 1) / experts;
+  auto items = [&](int BM, int BN) { return experts * ((avg + BM - 1) / BM) * ((lines + BN - 1) / BN); };
+  GatedTile tile;
+  long long n, slots = cus;  // tiles, and those that run at once
+  if (bf16) {
+    // 256 rows each of 8 experts, 4096 x 14336: gate and up 0.62, 128 x 256 0.69 ms (down 0.36 and 0.43)
+    if (avg > 112 && 4 * items(256, 256) >= 3 * cus) tile = kGated256x256x2, n = items(256, 256);
+    // 64 rows each of 8: 0.40, 256 x 256 0.47, 64 x 128 0.44 ms
+    else if (avg > 64 && 4 * items(128, 256) >= 3 * cus) tile = kGated128x256x3, n = items(128, 256);
+    // 83 rows each of 12, 1000 x 1720: down 27 (split in 2), 256 x 256 48, 64 x 128 24 us
+    else if (avg > 64) tile = kGated128x128x2, n = items(128, 128), slots = 2 * cus;
+    else if (avg > 32) tile = kGated64x128x3, n = items(64, 128), slots = 2 * cus;
+    // 8 rows each of 16, 4096 x 6400, 800 tiles: gate and up 273, with one block a CU and three stages 291 us
+    else if (items(32, 256) > cus) tile = kGated32x256x2, n = items(32, 256), slots = 2 * cus;
+    // one row of 2 experts, 4096 x 14336, 224 tiles: 82, with two stages 98 us
+    else tile = kGated32x256x3, n = items(32, 256);
+  } else {
+    // fp32's products take eight times as long, so it is their count that matters,
+    // rows past an expert's last among it: 4096 x 2048 x 8192: 1.01 ms (139 TFLOP/s), 64 x 128 1.10
+    if (avg > 512) tile = kGated128x128x2, n = items(128, 128), slots = 2 * cus;
+    // 207 rows each of 5, 1000 x 712: hidden gradients 35, 128 x 128 47 us (both split)
+    else if (avg > 112) tile = kGated64x128x3, n = items(64, 128), slots = 2 * cus;
+    // 83 rows each of 12, 1000 x 1720: gate and up 82, 128 x 128 131, 64 x 128 118 us
+    else tile = kGated32x128x2, n = items(32, 128), slots = 4 * cus;
+  }
+  // Too few tiles to fill the CUs share their reductions, at least four stages each:
+  // one row of 2 experts, 14336 x 4096: 50, unsplit 139 us; 2 rows of 512 x 1024 in fp32: 16 and 45 us.
+  long long splits = slots / n;
+  if (splits > stages / 4) splits = stages / 4;
+  if (splits > 32) splits = 32;
+  // Weights that few rows read, too large for the 256 MB last-level cache to hold until
+  // the next call: 8 rows each of 16, 1.7 GB: 292 -> 273 us; one of 2, 470 MB: 88 -> 82 us.
+  // Small ones, warm: 17.8 -> 21.4 us (1024 x 2048).
+  const bool once = bf16 && avg <= 32 && (long long)experts * lines * stages * 128 >= 128LL << 20;
+  return {tile, splits < 2 ? 1 : (int)splits, once};
 }
 
 }  // namespace moe

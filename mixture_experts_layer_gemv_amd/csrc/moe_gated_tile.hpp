@@ -16,6 +16,7 @@
 // operands, so nothing that lies there, NaN included, reaches a sum.
 #pragma once
 
+#include <cstddef>
 #include <type_traits>
 
 #include "moe_gated.hpp"
@@ -79,77 +80,123 @@ __device__ __forceinline__ f32x16_t multiply(f32x4_t w, f32x4_t x, f32x16_t acc)
   return acc;
 }
 
-// n stages of products into acc.  issue(s, j) copies part j of the wave's Sh::CP
-// of stage s.  The last stage holds `quarters` quarters of steps.
+// The stages of a reduction that a workgroup takes: [lo, hi) of TERMS reductions
+// of `per` stages, one after the other; with tail each one's last stage ends past
+// the reduction (is partial) and holds `quarters` quarters of steps.
+struct Stages {
+  int lo, hi, per;
+  bool tail;
+  int quarters;
+};
+__device__ __forceinline__ Stages stages_of(int K, int KD, int terms) {
+  const int per = (K + KD - 1) / KD, left = K - (per - 1) * KD;
+  return {0, per * terms, per, left != KD, (left + KD / 4 - 1) / (KD / 4)};
+}
+
+// The products of a workgroup's stages into acc.  at(s) is what the copies of stage
+// s start from; issue(at, slot, j, partial) makes copy j of the wave's Sh::CP.
+// live: the wave's row blocks that hold rows (an expert's last tile); the others are
+// not read or multiplied, and a wave without any only copies.
 //
 // Every operand read is issued ahead of the products of the quarter before it,
 // across the stages too: a stage's last quarter is multiplied after the barrier
 // that frees its ring slot, while the copies into that slot and the next stage's
 // first reads are under way; a read or copy follows each product, so that the
 // matrix cores do not wait for either to issue.
-template <class T, int TB, int CB, int WT, int WC, int S, bool XS, bool WS, bool GATED, class Issue>
-__device__ __forceinline__ void reduce_stages(f32x16_t (&acc)[CB][TB], const unsigned char* ring, int n, int quarters,
-                                              int wt, int wc, int lane, Issue issue) {
+template <class T, int TB, int CB, int WT, int WC, int S, bool XS, bool WS, bool GATED, int TERMS, int LIVE, class At, class Issue>
+__device__ __forceinline__ void reduce_live(f32x16_t (&acc)[CB][TB], const unsigned char* ring, const Stages& st, int wt,
+                                            int wc, int lane, At at, Issue issue) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   struct Frag {
-    typename T::Frag x[TB], w[CB];
+    typename T::Frag x[LIVE ? LIVE : 1], w[CB];
   };
-  if (n <= 0) return;
-  const int last = n - 1;
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (s <= last)
-#pragma unroll
-      for (int j = 0; j < Sh::CP; ++j) issue(s, j);
-  if (S - 1 <= last) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 1)));
-  else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-  ring_barrier();
+  const int n = st.hi - st.lo, last = n - 1;
   auto load_one = [&](Frag& f, int s, int ks, int j) {
-    const unsigned char* st = ring + (s % S) * (Sh::XB + Sh::WB);
-    if (j < CB) f.w[j] = read_operand<T, WS>(st + Sh::XB, channel_block(GATED, WC, CB, wc, j), ks, lane);
-    else f.x[j - CB] = read_operand<T, XS>(st, wt * TB + j - CB, ks, lane);
+    const unsigned char* slot = ring + (s % S) * (Sh::XB + Sh::WB);
+    if (j < CB) f.w[j] = read_operand<T, WS>(slot + Sh::XB, channel_block(GATED, WC, CB, wc, j), ks, lane);
+    else f.x[j - CB] = read_operand<T, XS>(slot, wt * TB + j - CB, ks, lane);
   };
-  constexpr int READS = CB + TB, PRODUCTS = TB * CB;
-  // The products of `f` between the reads of `next` (quarter ks of stage s) and,
-  // with COPY, the copies of stage cs.
-  auto pass = [&](const Frag& f, Frag& next, int s, int ks, auto copy, int cs) {
-    constexpr int COPIES = decltype(copy)::value ? Sh::CP : 0;
+  constexpr int READS = LIVE ? CB + LIVE : 0, PRODUCTS = LIVE * CB;
+  // The products of `f` between the reads of `next` (quarter ks of stage s) and
+  // the copies that `copy` makes.
+  auto pass = [&](const Frag& f, Frag& next, int s, int ks, auto copy) {
+    constexpr int COPIES = std::is_same<decltype(copy), std::nullptr_t>::value ? 0 : Sh::CP;
     constexpr int N = PRODUCTS > READS ? (PRODUCTS > COPIES ? PRODUCTS : COPIES) : (READS > COPIES ? READS : COPIES);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (j < READS) load_one(next, s, ks, j);
       if (j < PRODUCTS) acc[j % CB][j / CB] = multiply(f.w[j % CB], f.x[j / CB], acc[j % CB][j / CB]);
-      if (j < COPIES) issue(cs, j);
+      if constexpr (COPIES > 0)
+        if (j < COPIES) copy(j);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  const std::false_type none{};
   Frag f0, f1;
 #pragma unroll
   for (int j = 0; j < READS; ++j) load_one(f0, 0, 0, j);
-  int s = 0;
-  for (; s + S <= last; ++s) {
-    pass(f0, f1, s, 1, none, 0);
-    pass(f1, f0, s, 2, none, 0);
-    pass(f0, f1, s, 3, none, 0);
+  // stage c - S is multiplied while stage c is copied
+  auto turn = [&](int c, auto partial) {
+    const int s = c - S;
+    pass(f0, f1, s, 1, nullptr);
+    pass(f1, f0, s, 2, nullptr);
+    pass(f0, f1, s, 3, nullptr);
+    const auto a = at(st.lo + c);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 2)));
     ring_barrier();
-    pass(f1, f0, s + 1, 0, std::true_type{}, s + S);
+    pass(f1, f0, s + 1, 0, [&](int j) { issue(a, c % S, j, partial); });
+  };
+  int c = S;
+  for (int term = 1; term <= TERMS; ++term) {
+    const int whole = term * st.per - (st.tail ? 1 : 0) - st.lo, end = whole < n ? whole : n;
+    for (; c < end; ++c) turn(c, std::false_type{});
+    if (st.tail && c == whole && c < n) turn(c++, std::true_type{});
   }
-  for (; s < last; ++s) {
-    pass(f0, f1, s, 1, none, 0);
-    pass(f1, f0, s, 2, none, 0);
-    pass(f0, f1, s, 3, none, 0);
+  for (int s = c - S > 0 ? c - S : 0; s < last; ++s) {
+    pass(f0, f1, s, 1, nullptr);
+    pass(f1, f0, s, 2, nullptr);
+    pass(f0, f1, s, 3, nullptr);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     ring_barrier();
-    pass(f1, f0, s + 1, 0, none, 0);
+    pass(f1, f0, s + 1, 0, nullptr);
   }
+  const int quarters = st.hi % st.per ? 4 : st.quarters;
   for (int ks = 0; ks < quarters; ++ks) {
 #pragma unroll
     for (int j = 0; j < READS; ++j) load_one(f0, last, ks, j);
 #pragma unroll
     for (int j = 0; j < PRODUCTS; ++j) acc[j % CB][j / CB] = multiply(f0.w[j % CB], f0.x[j / CB], acc[j % CB][j / CB]);
   }
+}
+
+template <class T, int TB, int CB, int WT, int WC, int S, bool XS, bool WS, bool GATED, int TERMS, class At, class Issue>
+__device__ __forceinline__ void reduce_stages(f32x16_t (&acc)[CB][TB], const unsigned char* ring, const Stages& st, int live,
+                                              int wt, int wc, int lane, At at, Issue issue) {
+  using Sh = TileShape<TB, CB, WT, WC, S>;
+  const int n = st.hi - st.lo;
+  if (n <= 0) return;
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < n) {
+      const auto a = at(st.lo + s);
+      if (st.tail && (st.lo + s + 1) % st.per == 0) {
+#pragma unroll
+        for (int j = 0; j < Sh::CP; ++j) issue(a, s, j, std::true_type{});
+      } else {
+#pragma unroll
+        for (int j = 0; j < Sh::CP; ++j) issue(a, s, j, std::false_type{});
+      }
+    }
+  if (S <= n) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Sh::CP * (S - 1)));
+  else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  ring_barrier();
+  auto go = [&](auto l) {
+    reduce_live<T, TB, CB, WT, WC, S, XS, WS, GATED, TERMS, decltype(l)::value>(acc, ring, st, wt, wc, lane, at, issue);
+  };
+  if (live >= TB) go(std::integral_constant<int, TB>{});
+  else if (live <= 0) go(std::integral_constant<int, 0>{});
+  else if (TB == 4 && live == 3) go(std::integral_constant<int, TB == 4 ? 3 : 1>{});
+  else if (TB == 4 && live == 2) go(std::integral_constant<int, TB == 4 ? 2 : 1>{});
+  else go(std::integral_constant<int, 1>{});
 }
 
 // ---- epilogues ---------------------------------------------------------------------
@@ -253,10 +300,79 @@ __device__ __forceinline__ int2 expert_rows(const int32_t* offsets, int E, int R
 
 // ---- products over the experts' rows --------------------------------------------
 
-template <class T, Op OP, int TB, int CB, int WT, int WC, int S>
+// The outputs at element `at` from its sums (gated: a gate's, b up's).
+template <class T, Op OP>
+__device__ __forceinline__ void finish(const GatedArgs& A, size_t at, const Vec<T>& a, const Vec<T>& b) {
+  constexpr int V = Vec<T>::N;
+  if constexpr (OP == Op::kUp) {
+    Vec<T> h;
+#pragma unroll
+    for (int j = 0; j < V; ++j) h.v[j] = a.v[j] * sigmoid<T>(a.v[j]) * b.v[j];
+    store_vec<T>(A.out[0], at, h);
+    if (A.out[1]) store_vec<T>(A.out[1], at, a);
+    if (A.out[2]) store_vec<T>(A.out[2], at, b);
+  } else if constexpr (OP == Op::kGradHidden) {
+    // h = g s u with s = sigmoid(g): dg = dh u s (1 + g (1 - s)), du = dh g s
+    const Vec<T> g = load_vec<T>(A.in[0], at), u = load_vec<T>(A.in[1], at);
+    Vec<T> dg, du, h;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float s = sigmoid<T>(g.v[j]), gs = g.v[j] * s;
+      h.v[j] = gs * u.v[j];
+      du.v[j] = a.v[j] * gs;
+      dg.v[j] = a.v[j] * u.v[j] * (s + gs * (1.0f - s));
+    }
+    store_vec<T>(A.out[0], at, dg);
+    store_vec<T>(A.out[1], at, du);
+    if (A.out[2]) store_vec<T>(A.out[2], at, h);
+  } else {
+    store_vec<T>(A.out[0], at, a);
+  }
+}
+
+// Joins a split reduction: the partial sums added in order, then the outputs.
+// The experts' ranges follow one another (find_item), so a row has an expert if it
+// lies between the first range's start and the last one's end.
+template <class T, Op OP>
+__global__ __launch_bounds__(256) void k_gated_join(const GatedArgs A, int splits) {
+  constexpr int V = Vec<T>::N;
+  constexpr bool GATED = OP == Op::kUp;
+  int lo = 0, hi = A.R;
+  if (A.offsets) {
+    const int lane = threadIdx.x & 63;
+    lo = min(max(A.offsets[0], 0), A.R);
+    hi = min(max(A.offsets[min(lane, A.E)], 0), A.R);
+    hi = max(hi, min(max(A.offsets[A.E], 0), A.R));
+    for (int d = 1; d < 64; d <<= 1) hi = max(hi, __shfl_xor(hi, d, 64));
+  }
+  const int vecs = A.N / V, lines = GATED ? 2 * A.N : A.N;
+  const size_t step = (size_t)A.R * lines;
+  const long long n = (long long)(hi - lo) * vecs;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += 256LL * gridDim.x) {
+    const int r = lo + (int)(i / vecs), c = (int)(i % vecs) * V;
+    const float* p = A.part + (size_t)r * lines + c;
+    Vec<T> a = {}, b = {};
+    for (int k = 0; k < splits; ++k, p += step)
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const f32x4_t f = *reinterpret_cast<const f32x4_t*>(p + j);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a.v[j + v] += f[v];
+        if constexpr (GATED) {
+          const f32x4_t g = *reinterpret_cast<const f32x4_t*>(p + A.N + j);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) b.v[j + v] += g[v];
+        }
+      }
+    finish<T, OP>(A, (size_t)r * A.N + c, a, b);
+  }
+}
+
+// ONCE: the weights are not kept in the caches.
+template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE>
 __global__ __launch_bounds__(WT* WC * 64)
     __attribute__((amdgpu_waves_per_eu(TileShape<TB, CB, WT, WC, S>::per_simd, TileShape<TB, CB, WT, WC, S>::per_simd)))
-void k_gated_rows(const GatedArgs A, int cg) {
+void k_gated_rows(const GatedArgs A, int cg, int splits) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   constexpr bool GATED = OP == Op::kUp, WS = weights_by_step(OP), TWO = OP == Op::kGradX;
   constexpr int ES = T::ES, KD = stage_steps(ES);
@@ -267,57 +383,76 @@ void k_gated_rows(const GatedArgs A, int cg) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WC, wc = wave % WC;
-  const Item it = find_item(A.offsets, A.E, A.R, Sh::BM, (A.N + BN - 1) / BN, cg, (int)blockIdx.x, true);
+  const int items = (int)gridDim.x / splits, split = (int)blockIdx.x / items;
+  const Item it = find_item(A.offsets, A.E, A.R, Sh::BM, (A.N + BN - 1) / BN, cg, (int)blockIdx.x - split * items, true);
   if (it.e < 0) return;
   const int row0 = it.row0, rows = it.rows, n0 = it.nb * BN;
 
   // Copies: the lines past the tile's last row or column re-read the last one.
+  const int K = A.K, N = A.N;
   const char* xsrc[Sh::CPX];
   uint32_t wsrc[Sh::CPW];
 #pragma unroll
   for (int j = 0; j < Sh::CPX; ++j) {
-    int r = row0 + min(8 * (Sh::CPX * wave + j) + (lane >> 3), rows - 1);
+    const int i = Sh::CPX * wave + j;
+    int r = row0 + min(8 * i + (lane >> 3), rows - 1);
     if (A.perm) {
       const int t = A.perm[r] / A.topk;
       r = t < 0 ? 0 : (t >= A.T ? A.T - 1 : t);
     }
-    xsrc[j] = static_cast<const char*>(A.x) + (size_t)r * A.K * ES;
+    xsrc[j] = static_cast<const char*>(A.x) + (size_t)r * K * ES + 16 * chunk_of(i, lane);
   }
 #pragma unroll
   for (int j = 0; j < Sh::CPW; ++j) {
-    const int i = (8 * (Sh::CPW * wave + j) + (lane >> 3)) % (GATED ? Sh::BN / 2 : Sh::BN);
-    if (WS) wsrc[j] = (uint32_t)min((n0 + line_group(i, ES) * KD) * ES + 16 * step_chunk(lane), A.N * ES - 16) +
-                      (uint32_t)line_step(i, ES) * (uint32_t)(A.N * ES);
-    else wsrc[j] = (uint32_t)min(i, A.N - 1 - n0) * (uint32_t)(A.K * ES);
+    const int c = Sh::CPW * wave + j, i = (8 * c + (lane >> 3)) % (GATED ? Sh::BN / 2 : Sh::BN);
+    if (WS) wsrc[j] = (uint32_t)min((n0 + line_group(i, ES) * KD) * ES + 16 * step_chunk(lane), N * ES - 16) +
+                      (uint32_t)line_step(i, ES) * (uint32_t)(N * ES);
+    else wsrc[j] = (uint32_t)min(i, N - 1 - n0) * (uint32_t)(K * ES) + 16 * chunk_of(c, lane);
   }
-  const size_t wexpert = (size_t)it.e * A.K * A.N * ES;
   const uint32_t lds0 = lds_address(&ring[0]);
-  const int per = (A.K + KD - 1) / KD, n = TWO ? 2 * per : per;  // stages of a term, and in all
-  const bool tail = A.K % KD != 0;
+  Stages st = stages_of(K, KD, TWO ? 2 : 1);
+  if (splits > 1) {
+    const int all = st.hi;
+    st.lo = (int)((long long)all * split / splits);
+    st.hi = (int)((long long)all * (split + 1) / splits);
+  }
+  const size_t wstart = ((size_t)it.e * N * K + (WS ? 0 : (size_t)n0 * K)) * ES;
+  const char* const w0 = static_cast<const char*>(A.w[0]) + wstart;
+  const char* const w1 = GATED || TWO ? static_cast<const char*>(A.w[1]) + wstart : nullptr;
   const ptrdiff_t second = TWO ? static_cast<const char*>(A.x2) - static_cast<const char*>(A.x) : 0;
-  auto issue = [&](int s, int j) {
-    const int term = TWO && s >= per, k0 = (s - (term ? per : 0)) * KD;
-    const uint32_t at = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB);
-    const bool partial = tail && k0 + KD > A.K;
+  struct At {
+    const char *w, *up;  // the stage's weights (gated: gate's and up's)
+    ptrdiff_t x;         // and the offset of the rows' pointers
+    int k0;
+  };
+  auto at = [&](int s) {
+    const bool term = TWO && s >= st.per;
+    At a;
+    a.k0 = (s - (term ? st.per : 0)) * KD;
+    const size_t off = WS ? (size_t)a.k0 * N * ES : (size_t)a.k0 * ES;
+    a.w = (term ? w1 : w0) + off;
+    a.up = GATED ? w1 + off : nullptr;
+    a.x = (ptrdiff_t)a.k0 * ES + (term ? second : 0);
+    return a;
+  };
+  auto issue = [&](const At& a, int slot, int j, auto partial) {
+    constexpr bool PART = decltype(partial)::value;
+    const char* const zeros = reinterpret_cast<const char*>(g_zeros);
+    const uint32_t to = lds0 + (uint32_t)slot * (Sh::XB + Sh::WB);
     if (j < Sh::CPX) {
-      const int i = Sh::CPX * wave + j, b = k0 * ES + 16 * chunk_of(i, lane);
-      const char* p = xsrc[j] + b + (TWO && term ? second : 0);
-      if (partial && b >= A.K * ES) p = reinterpret_cast<const char*>(g_zeros);
-      copy_at(p, at + i * 1024);
+      const int i = Sh::CPX * wave + j;
+      const char* p = xsrc[j] + a.x;
+      if (PART && a.k0 * ES + 16 * chunk_of(i, lane) >= K * ES) p = zeros;
+      copy_at(p, to + i * 1024);
     } else {
       const int jw = j - Sh::CPX, i = Sh::CPW * wave + jw;
-      const bool up = GATED && 8 * i >= Sh::BN / 2;
-      const char* base = static_cast<const char*>(TWO ? A.w[term] : A.w[up ? 1 : 0]) + wexpert;
-      const uint32_t to = at + Sh::XB + i * 1024;
-      if (WS) {
-        base += (size_t)k0 * A.N * ES;
-        if (!partial) copy_frag(base, wsrc[jw], to);
-        else copy_at(k0 + line_step(8 * i + (lane >> 3), ES) < A.K ? base + wsrc[jw] : reinterpret_cast<const char*>(g_zeros), to);
+      const char* base = GATED && 8 * i >= Sh::BN / 2 ? a.up : a.w;
+      if constexpr (!PART) {
+        if constexpr (ONCE) copy_frag_once(base, wsrc[jw], to + Sh::XB + i * 1024);
+        else copy_frag(base, wsrc[jw], to + Sh::XB + i * 1024);
       } else {
-        base += (size_t)n0 * A.K * ES + (size_t)k0 * ES;
-        const int c = 16 * chunk_of(i, lane);
-        if (!partial) copy_frag(base, wsrc[jw] + c, to);
-        else copy_at(k0 * ES + c < A.K * ES ? base + wsrc[jw] + c : reinterpret_cast<const char*>(g_zeros), to);
+        const bool in = WS ? a.k0 + line_step(8 * i + (lane >> 3), ES) < K : a.k0 * ES + 16 * chunk_of(i, lane) < K * ES;
+        copy_at(in ? base + wsrc[jw] : zeros, to + Sh::XB + i * 1024);
       }
     }
   };
@@ -329,44 +464,31 @@ void k_gated_rows(const GatedArgs A, int cg) {
     for (int i = 0; i < TB; ++i)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.0f;
-  const int left = A.K - (per - 1) * KD;
-  reduce_stages<T, TB, CB, WT, WC, S, false, WS, GATED>(acc, ring, n, (left + KD / 4 - 1) / (KD / 4), wt, wc, lane, issue);
+  const int live = (rows - wt * TB * 32 + 31) >> 5;
+  reduce_stages<T, TB, CB, WT, WC, S, false, WS, GATED, TWO ? 2 : 1>(acc, ring, st, live, wt, wc, lane, at, issue);
   __syncthreads();  // the ring is free
 
-  constexpr int CH = GATED ? CB / 2 : CB, N = Vec<T>::N;
+  constexpr int CH = GATED ? CB / 2 : CB;
   unsigned char* const stage = ring + wave * 32 * (32 * CB * 4 + 16);
   const int nw = n0 + 32 * CH * wc;  // the wave's first output column
 #pragma unroll
   for (int i = 0; i < TB; ++i) {
     const int rb = (wt * TB + i) * 32;
     if (rb >= rows) break;
+    if (splits > 1) {  // fp32 partial sums, a row's gate and then its up
+      const int lines = GATED ? 2 * N : N;
+      float* const part = A.part + ((size_t)split * A.R + row0) * lines;
+      each_vec<F32, TB, CB, CB>(acc, i, stage, lane, [&](int r, int ch, const Vec<F32>& a, const Vec<F32>&) {
+        const int col = nw + (GATED ? ch % (32 * CH) : ch);
+        if (rb + r < rows && col < N)
+          store_vec<F32>(part, (size_t)(rb + r) * lines + col + (GATED && ch >= 32 * CH ? N : 0), a);
+      });
+      continue;
+    }
     each_vec<T, TB, CB, CH>(acc, i, stage, lane, [&](int r, int ch, const Vec<T>& a, const Vec<T>& b) {
-      if (rb + r >= rows || nw + ch >= A.N) return;
-      const size_t at = (size_t)(row0 + rb + r) * A.N + nw + ch;
-      if constexpr (OP == Op::kUp) {
-        Vec<T> h;
-#pragma unroll
-        for (int j = 0; j < N; ++j) h.v[j] = a.v[j] * sigmoid<T>(a.v[j]) * b.v[j];
-        store_vec<T>(A.out[0], at, h);
-        if (A.out[1]) store_vec<T>(A.out[1], at, a);
-        if (A.out[2]) store_vec<T>(A.out[2], at, b);
-      } else if constexpr (OP == Op::kGradHidden) {
-        // h = g s u with s = sigmoid(g): dg = dh u s (1 + g (1 - s)), du = dh g s
-        const Vec<T> g = load_vec<T>(A.in[0], at), u = load_vec<T>(A.in[1], at);
-        Vec<T> dg, du, h;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float s = sigmoid<T>(g.v[j]), gs = g.v[j] * s;
-          h.v[j] = gs * u.v[j];
-          du.v[j] = a.v[j] * gs;
-          dg.v[j] = a.v[j] * u.v[j] * (s + gs * (1.0f - s));
-        }
-        store_vec<T>(A.out[0], at, dg);
-        store_vec<T>(A.out[1], at, du);
-        if (A.out[2]) store_vec<T>(A.out[2], at, h);
-      } else {
-        store_vec<T>(A.out[0], at, a);
-      }
+      if (rb + r >= rows || nw + ch >= N) return;
+      const size_t at = (size_t)(row0 + rb + r) * N + nw + ch;
+      finish<T, OP>(A, at, a, b);
     });
   }
 }
@@ -384,17 +506,18 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WC, wc = wave % WC;
   // the item: expert, problem, tile
-  const int L = xcd_item((int)blockIdx.x, per_expert * A.E, 0);
-  if (L < 0) return;
-  const int e = L / per_expert;
-  int li = L - e * per_expert, q = 0, MB = 0, NB = 0;
+  const ExpertItem it = expert_item((int)blockIdx.x, per_expert);
+  const int e = it.e;
+  if (e >= A.E) return;
+  int li = it.tile, q = 0, MB = 0, NB = 0;
   for (;; ++q) {
     MB = (A.p[q].M + Sh::BM - 1) / Sh::BM;
     NB = (A.p[q].N + Sh::BN - 1) / Sh::BN;
     if (li < MB * NB || q + 1 >= A.n) break;
     li -= MB * NB;
   }
-  const GradWProblem& P = A.p[q];
+  const GradWProblem P = A.p[q];
+  const int M = P.M, N = P.N;
   const int g = li / (MB * cg), rem = li - g * MB * cg, gw = min(NB - g * cg, cg);
   const int m0 = rem / gw * Sh::BM, n0 = (g * cg + rem % gw) * Sh::BN;
   const int2 range = expert_rows(A.offsets, A.E, A.R, e);
@@ -404,25 +527,34 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
 #pragma unroll
   for (int j = 0; j < Sh::CPX; ++j) {
     const int i = 8 * (Sh::CPX * wave + j) + (lane >> 3);
-    xsrc[j] = (uint32_t)min((m0 + line_group(i, ES) * KD) * ES + 16 * step_chunk(lane), P.M * ES - 16) +
-              (uint32_t)line_step(i, ES) * (uint32_t)(P.M * ES);
+    xsrc[j] = (uint32_t)min((m0 + line_group(i, ES) * KD) * ES + 16 * step_chunk(lane), M * ES - 16) +
+              (uint32_t)line_step(i, ES) * (uint32_t)(M * ES);
   }
 #pragma unroll
   for (int j = 0; j < Sh::CPW; ++j) {
     const int i = 8 * (Sh::CPW * wave + j) + (lane >> 3);
-    wsrc[j] = (uint32_t)min((n0 + line_group(i, ES) * KD) * ES + 16 * step_chunk(lane), P.N * ES - 16) +
-              (uint32_t)line_step(i, ES) * (uint32_t)(P.N * ES);
+    wsrc[j] = (uint32_t)min((n0 + line_group(i, ES) * KD) * ES + 16 * step_chunk(lane), N * ES - 16) +
+              (uint32_t)line_step(i, ES) * (uint32_t)(N * ES);
   }
   const uint32_t lds0 = lds_address(&ring[0]);
-  auto issue = [&](int s, int j) {
+  const char* const x0 = static_cast<const char*>(P.x) + (size_t)lo * M * ES;
+  const char* const w0 = static_cast<const char*>(P.w) + (size_t)lo * N * ES;
+  struct At {
+    const char *x, *w;
+    int k0;
+  };
+  auto at = [&](int s) {
     const int k0 = s * KD;
+    return At{x0 + (size_t)k0 * M * ES, w0 + (size_t)k0 * N * ES, k0};
+  };
+  auto issue = [&](const At& a, int slot, int j, auto partial) {
     const bool x = j < Sh::CPX;
     const int i = x ? Sh::CPX * wave + j : Sh::CPW * wave + j - Sh::CPX;
-    const char* base = static_cast<const char*>(x ? P.x : P.w) + (size_t)(lo + k0) * (x ? P.M : P.N) * ES;
+    const char* const base = x ? a.x : a.w;
     const uint32_t from = x ? xsrc[x ? j : 0] : wsrc[x ? 0 : j - Sh::CPX];
-    const uint32_t to = lds0 + (uint32_t)(s % S) * (Sh::XB + Sh::WB) + (x ? 0 : Sh::XB) + i * 1024;
-    if (k0 + KD <= K) copy_frag(base, from, to);
-    else copy_at(k0 + line_step(8 * i + (lane >> 3), ES) < K ? base + from : reinterpret_cast<const char*>(g_zeros), to);
+    const uint32_t to = lds0 + (uint32_t)slot * (Sh::XB + Sh::WB) + (x ? 0 : Sh::XB) + i * 1024;
+    if constexpr (!decltype(partial)::value) copy_frag(base, from, to);
+    else copy_at(a.k0 + line_step(8 * i + (lane >> 3), ES) < K ? base + from : reinterpret_cast<const char*>(g_zeros), to);
   };
 
   f32x16_t acc[CB][TB];
@@ -432,19 +564,19 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
     for (int i = 0; i < TB; ++i)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.0f;
-  const int n = (K + KD - 1) / KD, left = K - (n - 1) * KD;
-  reduce_stages<T, TB, CB, WT, WC, S, true, true, false>(acc, ring, n, (left + KD / 4 - 1) / (KD / 4), wt, wc, lane, issue);
+  const int live = (M - m0 - wt * TB * 32 + 31) >> 5;
+  reduce_stages<T, TB, CB, WT, WC, S, true, true, false, 1>(acc, ring, stages_of(K, KD, 1), live, wt, wc, lane, at, issue);
   __syncthreads();
 
   unsigned char* const stage = ring + wave * 32 * (32 * CB * 4 + 16);
   const int nw = n0 + 32 * CB * wc;
-  const size_t out0 = (size_t)e * P.M * P.N;
+  const size_t out0 = (size_t)e * M * N;
 #pragma unroll
   for (int i = 0; i < TB; ++i) {
     const int rb = m0 + (wt * TB + i) * 32;
-    if (rb >= P.M) break;
+    if (rb >= M) break;
     each_vec<T, TB, CB, CB>(acc, i, stage, lane, [&](int r, int ch, const Vec<T>& a, const Vec<T>&) {
-      if (rb + r < P.M && nw + ch < P.N) store_vec<T>(P.out, out0 + (size_t)(rb + r) * P.N + nw + ch, a);
+      if (rb + r < M && nw + ch < N) store_vec<T>(P.out, out0 + (size_t)(rb + r) * N + nw + ch, a);
     });
   }
 }
@@ -456,26 +588,70 @@ inline long long row_blocks(const GatedArgs& a, int BM) {
   return a.offsets ? (long long)a.R / BM + (a.R < a.E ? a.R : a.E) : ((long long)a.R + BM - 1) / BM;
 }
 
-template <class T, Op OP, int TB, int CB, int WT, int WC, int S>
-hipError_t launch_tile(const GatedArgs& a, int cg, hipStream_t s) {
+template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE = false>
+hipError_t launch_tile(const GatedArgs& a, int cg, int splits, hipStream_t s) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   constexpr int BN = OP == Op::kUp ? Sh::BN / 2 : Sh::BN;
-  const long long blocks = row_blocks(a, Sh::BM) * ((a.N + BN - 1) / BN);
-  if ((blocks + 8) * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
-  k_gated_rows<T, OP, TB, CB, WT, WC, S><<<(unsigned)((blocks + 7) / 8 * 8), WT * WC * 64, 0, s>>>(a, cg);
+  const long long blocks = (row_blocks(a, Sh::BM) * ((a.N + BN - 1) / BN) + 7) / 8 * 8 * splits;
+  if (blocks * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
+  k_gated_rows<T, OP, TB, CB, WT, WC, S, ONCE><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, splits);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || splits == 1) return e;
+  const long long vecs = (long long)a.R * (a.N / Vec<T>::N), n = (vecs + 255) / 256;
+  k_gated_join<T, OP><<<(unsigned)(n < 1 << 20 ? n : 1 << 20), 256, 0, s>>>(a, splits);
   return hipGetLastError();
+}
+
+// The product with the tile that choose_gated names.
+template <class T, Op OP>
+hipError_t rows_product(const GatedArgs& a, int cus, hipStream_t s) {
+  constexpr int cg = 4;  // column blocks that share their rows in an XCD's L2
+  constexpr int KD = stage_steps(T::ES);
+  const GatedChoice c = choose_gated(T::ES == 2, a.R, OP == Op::kUp ? 2LL * a.N : a.N,
+                                     (a.K + KD - 1) / KD * (OP == Op::kGradX ? 2 : 1), a.E, cus);
+  if (c.splits > 1 && !a.part) return hipErrorInvalidValue;
+  if constexpr (T::ES == 2) {
+    switch (c.tile) {
+      case kGated256x256x2: return launch_tile<T, OP, 4, 2, 2, 4, 2>(a, cg, c.splits, s);
+      case kGated128x256x3: return launch_tile<T, OP, 2, 2, 2, 4, 3>(a, cg, c.splits, s);
+      case kGated128x128x2: return launch_tile<T, OP, 2, 2, 2, 2, 2>(a, cg, c.splits, s);
+      case kGated64x128x3: return launch_tile<T, OP, 1, 2, 2, 2, 3>(a, cg, c.splits, s);
+      case kGated32x256x2:
+        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 2, true>(a, cg, c.splits, s) : launch_tile<T, OP, 1, 2, 1, 4, 2>(a, cg, c.splits, s);
+      case kGated32x256x3:
+        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 3, true>(a, cg, c.splits, s) : launch_tile<T, OP, 1, 2, 1, 4, 3>(a, cg, c.splits, s);
+      default: return hipErrorInvalidValue;
+    }
+  }
+  switch (c.tile) {
+    case kGated128x128x2: return launch_tile<T, OP, 2, 2, 2, 2, 2>(a, cg, c.splits, s);
+    case kGated64x128x3: return launch_tile<T, OP, 1, 2, 2, 2, 3>(a, cg, c.splits, s);
+    case kGated32x128x2: return launch_tile<T, OP, 1, 2, 1, 2, 2>(a, cg, c.splits, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+inline long long grad_w_tiles(const GradWArgs& a, int BM, int BN) {
+  long long per = 0;
+  for (int i = 0; i < a.n; ++i) per += (long long)((a.p[i].M + BM - 1) / BM) * ((a.p[i].N + BN - 1) / BN);
+  return per;
 }
 
 template <class T, int TB, int CB, int WT, int WC, int S>
 hipError_t launch_grad_w_tile(const GradWArgs& a, int cg, hipStream_t s) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
-  long long per = 0;
-  for (int i = 0; i < a.n; ++i)
-    per += (long long)((a.p[i].M + Sh::BM - 1) / Sh::BM) * ((a.p[i].N + Sh::BN - 1) / Sh::BN);
-  const long long blocks = per * a.E;
-  if ((blocks + 8) * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
-  k_gated_grad_w<T, TB, CB, WT, WC, S><<<(unsigned)((blocks + 7) / 8 * 8), WT * WC * 64, 0, s>>>(a, cg, (int)per);
+  const long long per = grad_w_tiles(a, Sh::BM, Sh::BN);
+  const long long blocks = (per + 7) / 8 * 8 * a.E;
+  if (blocks * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
+  k_gated_grad_w<T, TB, CB, WT, WC, S><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, (int)per);
   return hipGetLastError();
+}
+
+template <class T>
+hipError_t grad_w_product(const GradWArgs& a, int cus, hipStream_t s) {
+  constexpr int cg = 4;
+  if constexpr (T::ES == 2)
+    if (grad_w_tiles(a, 256, 256) * a.E >= 2 * cus) return launch_grad_w_tile<T, 4, 2, 2, 4, 2>(a, cg, s);
+  return launch_grad_w_tile<T, 2, 2, 2, 2, 2>(a, cg, s);
 }
 
 }  // namespace

@@ -105,7 +105,22 @@ static void channels(int WC, int CB) {
   }
 }
 
+// Every (expert, tile) exactly once, and an XCD's experts in order.
+static void items(int E, int tiles) {
+  std::set<std::pair<int, int>> seen;
+  int before[8] = {};
+  for (int b = 0; b < 8 * ((tiles + 7) / 8) * E; ++b) {
+    const moe::ExpertItem it = moe::expert_item(b, tiles);
+    if (it.e >= E) continue;
+    CHECK(it.e >= before[b & 7] && it.tile >= 0 && it.tile < tiles && seen.insert({it.e, it.tile}).second, "block %d", b);
+    before[b & 7] = it.e;
+  }
+  CHECK((int)seen.size() == E * tiles, "%zu of %d x %d", seen.size(), E, tiles);
+}
+
 int main() {
+  for (int E : {1, 2, 16, 64})
+    for (int tiles : {1, 3, 7, 8, 9, 100, 1201}) items(E, tiles);
   for (int columns : {64, 128, 256}) {
     bf16(columns);
     fp32(columns);
