@@ -245,7 +245,17 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
       }
     }
     const float var = team_sum(q, NT, first, red[LAYER ? 1 : turn]) * inv_m;
-    const float r = 1.0f / sqrtf(var + A.eps);
+    float r = 1.0f / sqrtf(var + A.eps);
+    float rest = 0.0f;  // of r, to 40 bits: one step of Newton's method on r^-2 = var + eps
+    if constexpr (ADD) {
+      const float v = var + A.eps, q1 = v * r, e = fmaf(-q1, r, 1.0f) - fmaf(v, r, -q1) * r;
+      if (r > 0.0f && r < INFINITY && e > -1.0f && e < 1.0f) {
+        rest = 0.5f * r * e;
+        const float near = r + rest;
+        rest -= near - r;
+        r = near;
+      }
+    }
     if (tid == 0 && t < A.T) {
       if (LAYER && A.mean) A.mean[t] = mu;
       if (A.rstd) A.rstd[t] = r;
@@ -265,7 +275,10 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(const NormArgs A, int NT) {
       for (int v = 0; v < V; ++v)  // past the row's end gamma and beta are 0, and so is y
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          f[v][j] = LAYER ? fmaf(f[v][j] * r, g[v][j], b[v][j]) : f[v][j] * r * g[v][j];
+          // h = f r as a sum of two, so that y is rounded once: codes are rounded
+          // from it, and each error moves some of them over a tie
+          const float h = f[v][j] * r, low = fmaf(f[v][j], r, -h) + f[v][j] * rest;
+          f[v][j] = LAYER ? fmaf(h, g[v][j], fmaf(low, g[v][j], b[v][j])) : fmaf(h, g[v][j], low * g[v][j]);
           top = fmaxf(top, fabsf(f[v][j]));
         }
       if (A.out && t < A.T)

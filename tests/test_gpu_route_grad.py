@@ -65,7 +65,8 @@ def outputs(d):
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("T,m,E,k,aux", [(1, 8, 1, 1, False), (1, 64, 8, 2, False), (3, 136, 2, 2, True), (65, 1000, 33, 4, True),
                                          (130, 264, 8, 2, False), (257, 4096, 16, 3, True), (64, 8200, 64, 8, False),
-                                         (1111, 520, 5, 1, True), (5000, 128, 17, 2, False), (700, 2048, 64, 64, True)])
+                                         (1111, 520, 5, 1, True), (5000, 128, 17, 2, False), (700, 2048, 64, 64, True), (8192, 64, 8, 2, False),
+                                         (8193, 72, 4, 2, True), (20000, 136, 40, 3, False)])
 def test_route_backward(T, m, E, k, aux, dtype):
     log(f"route gradient {dtype} T={T} m={m} E={E} k={k} aux={aux}")
     d = make(T, m, E, k, dtype, aux)
