@@ -589,7 +589,9 @@ moe_status moe_add_norm_backward(const void* dy, const void* dsum, const void* s
  * every row r of expert e (offsets[e] <= r < offsets[e+1]), t = perm[r] / topk or
  * t = r without perm:
  *   g = x[t] w_gate[e];  u = x[t] w_up[e];  y_perm[r] = (SiLU(g) * u) w_down[e]
- * The hidden row SiLU(g) * u is rounded to dtype between the projections.
+ * The hidden row SiLU(g) * u is rounded to dtype between the projections; bf16
+ * ones of up to 32 rows an expert in the mean (rows / min(rows, E)) are kept in two
+ * bf16 parts, to 2^-16 of their value.
  *  x          device [T][m] in dtype (MOE_F32 or MOE_BF16), as all tensors here.
  *  w_gate, w_up   device [E][m][p].   w_down  device [E][p][m].  (moe_weights_create's w1, w_up, w2.)
  *  offsets    device int32 [E+1] from moe_dispatch, or NULL: E must be 1 and all rows
@@ -617,7 +619,8 @@ moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, c
  *   dg = dh u s (1 + g (1 - s)),   du = dh g s
  *   dx_perm[r] = dg w_gate[e]^T + du w_up[e]^T
  *   dw_gate[e] = sum_r x[t]^T dg,  dw_up[e] = sum_r x[t]^T du,  dw_down[e] = sum_r h^T dy_perm[r]
- * dh stays in fp32; dg, du and h are rounded to dtype as operands of the products.
+ * dh stays in fp32; dg, du and h are rounded as operands of the products, like the
+ * hidden row there.
  *  dy_perm    device [rows][m];  gate, up as moe_gated_ffn_forward left them.
  *  x, weights, offsets, perm and sizes   as there (x may be NULL without dw_gate).
  *  dx_perm    device [rows][m] or NULL; moe_permute_rows_backward sums it to the

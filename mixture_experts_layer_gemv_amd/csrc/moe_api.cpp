@@ -1904,11 +1904,14 @@ moe_status check_gated_sizes(int rows, int m, int p, int E) {
 size_t value_bytes(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
 // The block's workspace: the rows that one product hands to the next (forward: h;
-// backward: the gradients of gate and up, h, and x in row order), then the partial
-// sums of a split reduction, which the products use in turn.
+// backward: the gradients of gate and up, and h; then the low parts of these, if they
+// have them; backward: x in row order), then the partial sums of a split
+// reduction, which the products use in turn.
 struct GatedSpace {
   size_t hidden, rows, part;
-  size_t bytes(bool backward) const { return backward ? 3 * hidden + rows + part : hidden + part; }
+  bool low;
+  size_t handed(bool backward) const { return (backward ? 3 : 1) * (low ? 2 : 1) * hidden; }
+  size_t bytes(bool backward) const { return handed(backward) + (backward ? rows : 0) + part; }
 };
 GatedSpace gated_space(int dtype, int rows, int m, int p, int E, bool backward) {
   const size_t es = value_bytes(dtype);
@@ -1917,6 +1920,7 @@ GatedSpace gated_space(int dtype, int rows, int m, int p, int E, bool backward) 
   GatedSpace s;
   s.hidden = align256((size_t)rows * p * es);
   s.rows = align256((size_t)rows * m * es);
+  s.low = moe::gated_low_parts(bf16, rows, E);
   s.part = backward ? std::max(moe::gated_part_bytes(bf16, false, rows, m, p, E, 1, cus),
                                moe::gated_part_bytes(bf16, false, rows, p, m, E, 2, cus))
                     : std::max(moe::gated_part_bytes(bf16, true, rows, m, p, E, 1, cus),
@@ -2034,7 +2038,7 @@ moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, c
     return fail(MOE_ERR_INVALID_ARG, "x, the weights, y_perm, gate and up must be 16-byte aligned");
   const GatedSpace space = gated_space(dtype, rows, m, p, E, false);
   if (moe_status rc = check_space(workspace, ws_bytes, space.bytes(false))) return rc;
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + space.hidden);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + space.handed(false));
   const hipStream_t s = as_stream(stream);
   const bool bf16 = dtype == MOE_BF16;
   moe::GatedArgs a{};
@@ -2050,6 +2054,7 @@ moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, c
   a.K = m;
   a.N = p;
   a.out[0] = workspace;
+  a.low = space.low ? (ptrdiff_t)space.hidden : 0;
   a.part = part;
   a.out[1] = gate;
   a.out[2] = up;
@@ -2063,6 +2068,7 @@ moe_status moe_gated_ffn_forward(const void* x, int dtype, const void* w_gate, c
   d.K = p;
   d.N = m;
   d.out[0] = y_perm;
+  d.low = a.low;
   d.part = part;
   MOE_TRY_HIP(run("gated_down", s, [&] { return moe::launch_gated_down(d, bf16, device_cus(), s); }));
   return ok();
@@ -2086,6 +2092,7 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
   char* du = nullptr;
   char* h = nullptr;
   float* part = nullptr;
+  ptrdiff_t low = 0;
   const void* xr = x;  // x in row order
   if (rows > 0) {
     if (!dy_perm || !w_gate || !w_up || !w_down || !gate || !up || (dw_gate && !x))
@@ -2097,7 +2104,9 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
     dg = static_cast<char*>(workspace);
     du = dg + space.hidden;
     h = du + space.hidden;
-    part = reinterpret_cast<float*>(h + space.hidden + space.rows);
+    low = space.low ? (ptrdiff_t)(3 * space.hidden) : 0;
+    char* const rows_x = dg + space.handed(true);
+    part = reinterpret_cast<float*>(rows_x + space.rows);
     moe::GatedArgs a{};
     a.x = dy_perm;
     a.w[0] = w_down;
@@ -2111,10 +2120,10 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
     a.out[0] = dg;
     a.out[1] = du;
     a.out[2] = dw_down ? h : nullptr;
+    a.low = low;
     a.part = part;
     MOE_TRY_HIP(run("gated_grad_hidden", s, [&] { return moe::launch_gated_grad_hidden(a, bf16, device_cus(), s); }));
     if (dw_gate && perm) {
-      char* const rows_x = h + space.hidden;
       MOE_TRY_HIP(run("gather_rows", s, [&] {
         return moe::launch_gather_rows(x, perm, T, topk, rows, (long long)m * es, rows_x, s);
       }));
@@ -2127,10 +2136,10 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
     w.R = rows;
     w.E = E;
     if (dw_gate) {
-      w.p[w.n++] = {xr, dg, dw_gate, m, p};
-      w.p[w.n++] = {xr, du, dw_up, m, p};
+      w.p[w.n++] = {xr, dg, low ? xr : nullptr, low ? dg + low : nullptr, dw_gate, m, p};
+      w.p[w.n++] = {xr, du, low ? xr : nullptr, low ? du + low : nullptr, dw_up, m, p};
     }
-    if (dw_down) w.p[w.n++] = {h, dy_perm, dw_down, p, m};
+    if (dw_down) w.p[w.n++] = {h, dy_perm, low ? h + low : nullptr, low ? dy_perm : nullptr, dw_down, p, m};
     MOE_TRY_HIP(run("gated_grad_w", s, [&] { return moe::launch_gated_grad_w(w, bf16, device_cus(), s); }));
   }
   if (dx_perm && rows > 0) {
@@ -2145,6 +2154,7 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
     a.K = p;
     a.N = m;
     a.out[0] = dx_perm;
+    a.low = low;
     a.part = part;
     MOE_TRY_HIP(run("gated_grad_x", s, [&] { return moe::launch_gated_grad_x(a, bf16, device_cus(), s); }));
   }

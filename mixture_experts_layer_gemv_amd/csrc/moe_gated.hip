@@ -34,6 +34,8 @@ hipError_t launch_gather_rows(const void* x, const int32_t* perm, int T, int top
   return hipGetLastError();
 }
 
+bool gated_low_parts(bool bf16, int R, int E) { return gated_pairs(bf16, R, E); }
+
 size_t gated_part_bytes(bool bf16, bool gated, int R, int K, int N, int E, int terms, int cus) {
   if (R <= 0) return 0;
   const long long lines = gated ? 2LL * N : N;

@@ -24,16 +24,20 @@ struct GatedArgs {
   int R, E, K, N;          // rows, experts, reduction, output columns
   void* out[3];
   const void* in[2];       // gate, up [R][N] (gradient of the hidden rows)
+  ptrdiff_t low;           // bytes from hidden rows to their low parts (gated_pairs), or 0: they have none
   float* part;             // workspace of a split reduction (gated_part_bytes), or null: none is split
 };
+// Whether R hidden rows of E experts are kept in two bf16 parts.
+bool gated_low_parts(bool bf16, int R, int E);
 // Bytes of `part` for a product of R rows with N output columns, by a reduction of K.
 size_t gated_part_bytes(bool bf16, bool gated, int R, int K, int N, int E, int terms, int cus);
 
 // The products with a weight gradient: out [E][M][N] = sum over an expert's
-// rows r of x[r][i] w[r][j].
+// rows r of x[r][i] w[r][j] (+ x2[r][i] w2[r][j]).
 struct GradWProblem {
   const void* x;  // [R][M]
   const void* w;  // [R][N]
+  const void *x2, *w2;  // the second term's, if an operand has a low part; else null
   void* out;
   int M, N;
 };

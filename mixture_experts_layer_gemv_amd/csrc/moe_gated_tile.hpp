@@ -80,6 +80,11 @@ __device__ __forceinline__ f32x16_t multiply(f32x4_t w, f32x4_t x, f32x16_t acc)
   return acc;
 }
 
+// A tile's buffers.  PAIR: each of its 32 rows has two lines, the high and the low part
+// of its values.
+template <int TB, int CB, int WT, int WC, int S, bool PAIR>
+using RowsShape = TileShape<PAIR ? 2 : TB, CB, WT, WC, S>;
+
 // The stages of a reduction that a workgroup takes: [lo, hi) of TERMS reductions
 // of `per` stages, one after the other; with tail each one's last stage ends past
 // the reduction (is partial) and holds `quarters` quarters of steps.
@@ -103,12 +108,13 @@ __device__ __forceinline__ Stages stages_of(int K, int KD, int terms) {
 // that frees its ring slot, while the copies into that slot and the next stage's
 // first reads are under way; a read or copy follows each product, so that the
 // matrix cores do not wait for either to issue.
-template <class T, int TB, int CB, int WT, int WC, int S, bool XS, bool WS, bool GATED, int TERMS, int LIVE, class At, class Issue>
+template <class T, int TB, int CB, int WT, int WC, int S, bool XS, bool WS, bool GATED, bool PAIR, int TERMS, int LIVE, class At, class Issue>
 __device__ __forceinline__ void reduce_live(f32x16_t (&acc)[CB][TB], const unsigned char* ring, const Stages& st, int wt,
                                             int wc, int lane, At at, Issue issue) {
-  using Sh = TileShape<TB, CB, WT, WC, S>;
+  using Sh = RowsShape<TB, CB, WT, WC, S, PAIR>;
+  constexpr int XB = PAIR ? 2 : LIVE;  // operands of rows; a pair's are multiplied into the same sums
   struct Frag {
-    typename T::Frag x[LIVE ? LIVE : 1], w[CB];
+    typename T::Frag x[XB ? XB : 1], w[CB];
   };
   const int n = st.hi - st.lo, last = n - 1;
   auto load_one = [&](Frag& f, int s, int ks, int j) {
@@ -116,7 +122,11 @@ __device__ __forceinline__ void reduce_live(f32x16_t (&acc)[CB][TB], const unsig
     if (j < CB) f.w[j] = read_operand<T, WS>(slot + Sh::XB, channel_block(GATED, WC, CB, wc, j), ks, lane);
     else f.x[j - CB] = read_operand<T, XS>(slot, wt * TB + j - CB, ks, lane);
   };
-  constexpr int READS = LIVE ? CB + LIVE : 0, PRODUCTS = LIVE * CB;
+  constexpr int READS = XB ? CB + XB : 0, PRODUCTS = XB * CB;
+  auto product = [&](const Frag& f, int j) {
+    f32x16_t& sum = acc[j % CB][PAIR ? 0 : j / CB];
+    sum = multiply(f.w[j % CB], f.x[j / CB], sum);
+  };
   // The products of `f` between the reads of `next` (quarter ks of stage s) and
   // the copies that `copy` makes.
   auto pass = [&](const Frag& f, Frag& next, int s, int ks, auto copy) {
@@ -125,7 +135,7 @@ __device__ __forceinline__ void reduce_live(f32x16_t (&acc)[CB][TB], const unsig
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (j < READS) load_one(next, s, ks, j);
-      if (j < PRODUCTS) acc[j % CB][j / CB] = multiply(f.w[j % CB], f.x[j / CB], acc[j % CB][j / CB]);
+      if (j < PRODUCTS) product(f, j);
       if constexpr (COPIES > 0)
         if (j < COPIES) copy(j);
       __builtin_amdgcn_sched_barrier(0);
@@ -164,14 +174,14 @@ __device__ __forceinline__ void reduce_live(f32x16_t (&acc)[CB][TB], const unsig
 #pragma unroll
     for (int j = 0; j < READS; ++j) load_one(f0, last, ks, j);
 #pragma unroll
-    for (int j = 0; j < PRODUCTS; ++j) acc[j % CB][j / CB] = multiply(f0.w[j % CB], f0.x[j / CB], acc[j % CB][j / CB]);
+    for (int j = 0; j < PRODUCTS; ++j) product(f0, j);
   }
 }
 
-template <class T, int TB, int CB, int WT, int WC, int S, bool XS, bool WS, bool GATED, int TERMS, class At, class Issue>
+template <class T, int TB, int CB, int WT, int WC, int S, bool XS, bool WS, bool GATED, bool PAIR, int TERMS, class At, class Issue>
 __device__ __forceinline__ void reduce_stages(f32x16_t (&acc)[CB][TB], const unsigned char* ring, const Stages& st, int live,
                                               int wt, int wc, int lane, At at, Issue issue) {
-  using Sh = TileShape<TB, CB, WT, WC, S>;
+  using Sh = RowsShape<TB, CB, WT, WC, S, PAIR>;
   const int n = st.hi - st.lo;
   if (n <= 0) return;
 #pragma unroll
@@ -190,9 +200,9 @@ __device__ __forceinline__ void reduce_stages(f32x16_t (&acc)[CB][TB], const uns
   else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   ring_barrier();
   auto go = [&](auto l) {
-    reduce_live<T, TB, CB, WT, WC, S, XS, WS, GATED, TERMS, decltype(l)::value>(acc, ring, st, wt, wc, lane, at, issue);
+    reduce_live<T, TB, CB, WT, WC, S, XS, WS, GATED, PAIR, TERMS, decltype(l)::value>(acc, ring, st, wt, wc, lane, at, issue);
   };
-  if (live >= TB) go(std::integral_constant<int, TB>{});
+  if (PAIR || live >= TB) go(std::integral_constant<int, TB>{});
   else if (live <= 0) go(std::integral_constant<int, 0>{});
   else if (TB == 4 && live == 3) go(std::integral_constant<int, TB == 4 ? 3 : 1>{});
   else if (TB == 4 && live == 2) go(std::integral_constant<int, TB == 4 ? 2 : 1>{});
@@ -235,6 +245,23 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const Vec<T>& f) {
       r[j] = __float_as_uint(f.v[j]);
   }
   *reinterpret_cast<u32x4_t*>(static_cast<char*>(p) + i * T::ES) = r;
+}
+
+// With `low`, what the rounding of f takes off as well, `low` bytes further on: the
+// two parts hold 16 bits of a value.
+template <class T>
+__device__ __forceinline__ void store_parts(void* p, size_t i, const Vec<T>& f, ptrdiff_t low) {
+  store_vec<T>(p, i, f);
+  if constexpr (T::ES == 2) {
+    if (!low) return;
+    Vec<T> rest;
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) {
+      const float high = (float)(__bf16)f.v[j];
+      rest.v[j] = fabsf(high) < INFINITY ? f.v[j] - high : 0.0f;
+    }
+    store_vec<T>(static_cast<char*>(p) + low, i, rest);
+  }
 }
 
 // 1 / (1 + exp(-g)).  In bf16 the fast exponential and reciprocal, good to 2^-21,
@@ -308,7 +335,7 @@ __device__ __forceinline__ void finish(const GatedArgs& A, size_t at, const Vec<
     Vec<T> h;
 #pragma unroll
     for (int j = 0; j < V; ++j) h.v[j] = a.v[j] * sigmoid<T>(a.v[j]) * b.v[j];
-    store_vec<T>(A.out[0], at, h);
+    store_parts<T>(A.out[0], at, h, A.low);
     if (A.out[1]) store_vec<T>(A.out[1], at, a);
     if (A.out[2]) store_vec<T>(A.out[2], at, b);
   } else if constexpr (OP == Op::kGradHidden) {
@@ -322,9 +349,9 @@ __device__ __forceinline__ void finish(const GatedArgs& A, size_t at, const Vec<
       du.v[j] = a.v[j] * gs;
       dg.v[j] = a.v[j] * u.v[j] * (s + gs * (1.0f - s));
     }
-    store_vec<T>(A.out[0], at, dg);
-    store_vec<T>(A.out[1], at, du);
-    if (A.out[2]) store_vec<T>(A.out[2], at, h);
+    store_parts<T>(A.out[0], at, dg, A.low);
+    store_parts<T>(A.out[1], at, du, A.low);
+    if (A.out[2]) store_parts<T>(A.out[2], at, h, A.low);
   } else {
     store_vec<T>(A.out[0], at, a);
   }
@@ -368,12 +395,16 @@ __global__ __launch_bounds__(256) void k_gated_join(const GatedArgs A, int split
   }
 }
 
-// ONCE: the weights are not kept in the caches.
-template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE>
+// ONCE: the weights are not kept in the caches.  PAIR: the rows come in two parts
+// (GatedArgs::low), whose products the same sums take.
+template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE, bool PAIR>
 __global__ __launch_bounds__(WT* WC * 64)
-    __attribute__((amdgpu_waves_per_eu(TileShape<TB, CB, WT, WC, S>::per_simd, TileShape<TB, CB, WT, WC, S>::per_simd)))
+    __attribute__((amdgpu_waves_per_eu(RowsShape<TB, CB, WT, WC, S, PAIR>::per_simd,
+                                       RowsShape<TB, CB, WT, WC, S, PAIR>::per_simd)))
 void k_gated_rows(const GatedArgs A, int cg, int splits) {
-  using Sh = TileShape<TB, CB, WT, WC, S>;
+  using Sh = RowsShape<TB, CB, WT, WC, S, PAIR>;
+  static_assert(!PAIR || (TB == 1 && WT == 1), "the pair's lines follow one another");
+  constexpr int BM = 32 * TB * WT;  // rows of a tile
   constexpr bool GATED = OP == Op::kUp, WS = weights_by_step(OP), TWO = OP == Op::kGradX;
   constexpr int ES = T::ES, KD = stage_steps(ES);
   constexpr int BN = GATED ? Sh::BN / 2 : Sh::BN;  // output columns of a tile
@@ -384,7 +415,7 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WC, wc = wave % WC;
   const int items = (int)gridDim.x / splits, split = (int)blockIdx.x / items;
-  const Item it = find_item(A.offsets, A.E, A.R, Sh::BM, (A.N + BN - 1) / BN, cg, (int)blockIdx.x - split * items, true);
+  const Item it = find_item(A.offsets, A.E, A.R, BM, (A.N + BN - 1) / BN, cg, (int)blockIdx.x - split * items, true);
   if (it.e < 0) return;
   const int row0 = it.row0, rows = it.rows, n0 = it.nb * BN;
 
@@ -395,12 +426,13 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
 #pragma unroll
   for (int j = 0; j < Sh::CPX; ++j) {
     const int i = Sh::CPX * wave + j;
-    int r = row0 + min(8 * i + (lane >> 3), rows - 1);
+    int r = row0 + min((8 * i + (lane >> 3)) % BM, rows - 1);
     if (A.perm) {
       const int t = A.perm[r] / A.topk;
       r = t < 0 ? 0 : (t >= A.T ? A.T - 1 : t);
     }
     xsrc[j] = static_cast<const char*>(A.x) + (size_t)r * K * ES + 16 * chunk_of(i, lane);
+    if (PAIR && 8 * i >= BM) xsrc[j] += A.low;
   }
 #pragma unroll
   for (int j = 0; j < Sh::CPW; ++j) {
@@ -465,7 +497,7 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.0f;
   const int live = (rows - wt * TB * 32 + 31) >> 5;
-  reduce_stages<T, TB, CB, WT, WC, S, false, WS, GATED, TWO ? 2 : 1>(acc, ring, st, live, wt, wc, lane, at, issue);
+  reduce_stages<T, TB, CB, WT, WC, S, false, WS, GATED, PAIR, TWO ? 2 : 1>(acc, ring, st, live, wt, wc, lane, at, issue);
   __syncthreads();  // the ring is free
 
   constexpr int CH = GATED ? CB / 2 : CB;
@@ -495,7 +527,8 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
 
 // ---- weight gradients ----------------------------------------------------------------
 
-template <class T, int TB, int CB, int WT, int WC, int S>
+// PAIR: the hidden operand comes in two parts (GradWProblem::x2, w2), a reduction each.
+template <class T, int TB, int CB, int WT, int WC, int S, bool PAIR>
 __global__ __launch_bounds__(WT* WC * 64)
     __attribute__((amdgpu_waves_per_eu(TileShape<TB, CB, WT, WC, S>::per_simd, TileShape<TB, CB, WT, WC, S>::per_simd)))
 void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
@@ -537,15 +570,19 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
               (uint32_t)line_step(i, ES) * (uint32_t)(N * ES);
   }
   const uint32_t lds0 = lds_address(&ring[0]);
+  const Stages st = stages_of(K, KD, PAIR ? 2 : 1);
   const char* const x0 = static_cast<const char*>(P.x) + (size_t)lo * M * ES;
   const char* const w0 = static_cast<const char*>(P.w) + (size_t)lo * N * ES;
+  const char* const x1 = PAIR ? static_cast<const char*>(P.x2) + (size_t)lo * M * ES : nullptr;
+  const char* const w1 = PAIR ? static_cast<const char*>(P.w2) + (size_t)lo * N * ES : nullptr;
   struct At {
     const char *x, *w;
     int k0;
   };
   auto at = [&](int s) {
-    const int k0 = s * KD;
-    return At{x0 + (size_t)k0 * M * ES, w0 + (size_t)k0 * N * ES, k0};
+    const bool second = PAIR && s >= st.per;
+    const int k0 = (s - (second ? st.per : 0)) * KD;
+    return At{(second ? x1 : x0) + (size_t)k0 * M * ES, (second ? w1 : w0) + (size_t)k0 * N * ES, k0};
   };
   auto issue = [&](const At& a, int slot, int j, auto partial) {
     const bool x = j < Sh::CPX;
@@ -565,7 +602,7 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.0f;
   const int live = (M - m0 - wt * TB * 32 + 31) >> 5;
-  reduce_stages<T, TB, CB, WT, WC, S, true, true, false, 1>(acc, ring, stages_of(K, KD, 1), live, wt, wc, lane, at, issue);
+  reduce_stages<T, TB, CB, WT, WC, S, true, true, false, false, PAIR ? 2 : 1>(acc, ring, st, live, wt, wc, lane, at, issue);
   __syncthreads();
 
   unsigned char* const stage = ring + wave * 32 * (32 * CB * 4 + 16);
@@ -588,13 +625,12 @@ inline long long row_blocks(const GatedArgs& a, int BM) {
   return a.offsets ? (long long)a.R / BM + (a.R < a.E ? a.R : a.E) : ((long long)a.R + BM - 1) / BM;
 }
 
-template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE = false>
+template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE = false, bool PAIR = false>
 hipError_t launch_tile(const GatedArgs& a, int cg, int splits, hipStream_t s) {
-  using Sh = TileShape<TB, CB, WT, WC, S>;
-  constexpr int BN = OP == Op::kUp ? Sh::BN / 2 : Sh::BN;
-  const long long blocks = (row_blocks(a, Sh::BM) * ((a.N + BN - 1) / BN) + 7) / 8 * 8 * splits;
+  constexpr int BM = 32 * TB * WT, BN = 32 * CB * WC / (OP == Op::kUp ? 2 : 1);
+  const long long blocks = (row_blocks(a, BM) * ((a.N + BN - 1) / BN) + 7) / 8 * 8 * splits;
   if (blocks * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
-  k_gated_rows<T, OP, TB, CB, WT, WC, S, ONCE><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, splits);
+  k_gated_rows<T, OP, TB, CB, WT, WC, S, ONCE, PAIR><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, splits);
   if (hipError_t e = hipGetLastError(); e != hipSuccess || splits == 1) return e;
   const long long vecs = (long long)a.R * (a.N / Vec<T>::N), n = (vecs + 255) / 256;
   k_gated_join<T, OP><<<(unsigned)(n < 1 << 20 ? n : 1 << 20), 256, 0, s>>>(a, splits);
@@ -609,6 +645,8 @@ hipError_t rows_product(const GatedArgs& a, int cus, hipStream_t s) {
   const GatedChoice c = choose_gated(T::ES == 2, a.R, OP == Op::kUp ? 2LL * a.N : a.N,
                                      (a.K + KD - 1) / KD * (OP == Op::kGradX ? 2 : 1), a.E, cus);
   if (c.splits > 1 && !a.part) return hipErrorInvalidValue;
+  constexpr bool PAIR = T::ES == 2 && (OP == Op::kDown || OP == Op::kGradX);  // the 32-row tiles of hidden rows
+  if (T::ES == 2 && (gated_pairs(true, a.R, a.E) != (a.low != 0))) return hipErrorInvalidValue;
   if constexpr (T::ES == 2) {
     switch (c.tile) {
       case kGated256x256x2: return launch_tile<T, OP, 4, 2, 2, 4, 2>(a, cg, c.splits, s);
@@ -616,9 +654,11 @@ hipError_t rows_product(const GatedArgs& a, int cus, hipStream_t s) {
       case kGated128x128x2: return launch_tile<T, OP, 2, 2, 2, 2, 2>(a, cg, c.splits, s);
       case kGated64x128x3: return launch_tile<T, OP, 1, 2, 2, 2, 3>(a, cg, c.splits, s);
       case kGated32x256x2:
-        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 2, true>(a, cg, c.splits, s) : launch_tile<T, OP, 1, 2, 1, 4, 2>(a, cg, c.splits, s);
+        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 2, true, PAIR>(a, cg, c.splits, s)
+                      : launch_tile<T, OP, 1, 2, 1, 4, 2, false, PAIR>(a, cg, c.splits, s);
       case kGated32x256x3:
-        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 3, true>(a, cg, c.splits, s) : launch_tile<T, OP, 1, 2, 1, 4, 3>(a, cg, c.splits, s);
+        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 3, true, PAIR>(a, cg, c.splits, s)
+                      : launch_tile<T, OP, 1, 2, 1, 4, 3, false, PAIR>(a, cg, c.splits, s);
       default: return hipErrorInvalidValue;
     }
   }
@@ -636,22 +676,27 @@ inline long long grad_w_tiles(const GradWArgs& a, int BM, int BN) {
   return per;
 }
 
-template <class T, int TB, int CB, int WT, int WC, int S>
+template <class T, int TB, int CB, int WT, int WC, int S, bool PAIR>
 hipError_t launch_grad_w_tile(const GradWArgs& a, int cg, hipStream_t s) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   const long long per = grad_w_tiles(a, Sh::BM, Sh::BN);
   const long long blocks = (per + 7) / 8 * 8 * a.E;
   if (blocks * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
-  k_gated_grad_w<T, TB, CB, WT, WC, S><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, (int)per);
+  k_gated_grad_w<T, TB, CB, WT, WC, S, PAIR><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, (int)per);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t grad_w_product(const GradWArgs& a, int cus, hipStream_t s) {
   constexpr int cg = 4;
-  if constexpr (T::ES == 2)
-    if (grad_w_tiles(a, 256, 256) * a.E >= 2 * cus) return launch_grad_w_tile<T, 4, 2, 2, 4, 2>(a, cg, s);
-  return launch_grad_w_tile<T, 2, 2, 2, 2, 2>(a, cg, s);
+  if constexpr (T::ES == 2) {
+    bool pair = true;
+    for (int i = 0; i < a.n; ++i) pair = pair && a.p[i].x2 && a.p[i].w2;
+    if (grad_w_tiles(a, 256, 256) * a.E >= 2 * cus)
+      return pair ? launch_grad_w_tile<T, 4, 2, 2, 4, 2, true>(a, cg, s) : launch_grad_w_tile<T, 4, 2, 2, 4, 2, false>(a, cg, s);
+    if (pair) return launch_grad_w_tile<T, 2, 2, 2, 2, 2, true>(a, cg, s);
+  }
+  return launch_grad_w_tile<T, 2, 2, 2, 2, 2, false>(a, cg, s);
 }
 
 }  // namespace

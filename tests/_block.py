@@ -2,15 +2,24 @@
 counts its roundings (torch tensors in float64, on whatever device).
 
 u = 2^-24 is half an fp32 step, U[dtype] half a step of the stored type.  A sum of n
-products on the matrix cores is within 2 n u sum|terms| of its exact value: each
-of its additions, in any order, is rounded or truncated to fp32 (at most a whole step, 2
-u).  sigmoid(g): exp(-g) carries its argument's rounding, |g| u, and its own steps,
+products on the matrix cores is within 2 n u sum|terms| of its exact value: each of its
+additions, in any order, is rounded or truncated to fp32 (at most a whole step, 2 u);
+values in two parts make twice as many products.  sigmoid(g): exp(-g) carries its argument's rounding, |g| u, and its own steps,
 the sum and the division or reciprocal one each: within (2 |g| + 8) u of its value.
 """
 import torch
 
 u = 2.0**-24
 U = {torch.float32: 2.0**-24, torch.bfloat16: 2.0**-8}
+
+
+def hidden_step(rows, E, dtype):
+    """Half a step of a hidden row's values: in bf16, two parts for up to 32 rows an expert,
+    the second rounded to half a step of what the first leaves (at most 2^-8 of the value)."""
+    few = rows and -(-rows // min(rows, E)) <= 32
+    return 2.0**-16 if dtype == torch.bfloat16 and few else U[dtype]
+
+
 TINY = 1e-36  # results and terms below the normal range round absolutely
 
 
@@ -38,7 +47,7 @@ def forward(x, wg, wu, wd, offsets, perm, topk, rows, dtype):
     y = torch.full((rows, m), float("nan"), dtype=torch.float64, device=x.device)
     g, up = (torch.full((rows, p), float("nan"), dtype=torch.float64, device=x.device) for _ in range(2))
     by, bg, bu = torch.zeros_like(y), torch.zeros_like(g), torch.zeros_like(up)
-    r_ = U[dtype]
+    r_, h_ = U[dtype], hidden_step(rows, E, dtype)
     for e, (lo, hi) in enumerate(ranges(offsets, rows, E)):
         if lo == hi:
             continue
@@ -52,10 +61,10 @@ def forward(x, wg, wu, wd, offsets, perm, topk, rows, dtype):
         s = torch.sigmoid(ge)
         h = ge * s * ue
         # silu' lies in (-0.1, 1.1); the sigmoid's error and two products
-        eh = 1.1 * eg * (ue.abs() + eu) + (ge * s).abs() * eu + h.abs() * (2 * ge.abs() + 12) * u + r_ * h.abs()
+        eh = 1.1 * eg * (ue.abs() + eu) + (ge * s).abs() * eu + h.abs() * (2 * ge.abs() + 12) * u + h_ * h.abs()
         ye, ya = _mm(h, W[2])
         y[lo:hi], g[lo:hi], up[lo:hi] = ye, ge, ue
-        by[lo:hi] = eh @ W[2].abs() + 2 * (p + 1) * u * ya + r_ * ye.abs()
+        by[lo:hi] = eh @ W[2].abs() + 2 * (2 * p + 1) * u * ya + r_ * ye.abs()
         bg[lo:hi], bu[lo:hi] = eg + r_ * ge.abs(), eu + r_ * ue.abs()
     return (y, g, up), (by, bg, bu)
 
@@ -66,7 +75,7 @@ def backward(dy, x, wg, wu, wd, gate, up, offsets, perm, topk, rows, dtype):
     dx = torch.full((rows, m), float("nan"), dtype=torch.float64, device=x.device)
     out = [dx] + [torch.zeros(w.shape, dtype=torch.float64, device=x.device) for w in (wg, wu, wd)]
     bnd = [torch.zeros_like(o) for o in out]
-    r_ = U[dtype]
+    r_, h_ = U[dtype], hidden_step(rows, E, dtype)
     for e, (lo, hi) in enumerate(ranges(offsets, rows, E)):
         if lo == hi:
             continue
@@ -83,16 +92,16 @@ def backward(dy, x, wg, wu, wd, gate, up, offsets, perm, topk, rows, dtype):
         a = q.abs() * (s + gs.abs() * (1 - s))  # bounds the factor of dg and its terms
         dg, du, h = dh * q * (s + gs * (1 - s)), dh * gs, gs * q
         near = (2 * g.abs() + 16) * u
-        edg = a * edh + (dh.abs() + edh) * a * near + r_ * dg.abs() * (1 + r_)
-        edu = gs.abs() * edh + (dh.abs() + edh) * gs.abs() * near + r_ * du.abs() * (1 + r_)
-        eh = h.abs() * near + r_ * h.abs()
+        edg = a * edh + (dh.abs() + edh) * a * near + h_ * dg.abs() * (1 + h_)
+        edu = gs.abs() * edh + (dh.abs() + edh) * gs.abs() * near + h_ * du.abs() * (1 + h_)
+        eh = h.abs() * near + h_ * h.abs()
         x1, a1 = _mm(dg, W[0].T)
         x2, a2 = _mm(du, W[1].T)
         out[0][lo:hi] = x1 + x2
-        bnd[0][lo:hi] = edg @ W[0].abs().T + edu @ W[1].abs().T + 2 * (2 * p + 1) * u * (a1 + a2) + r_ * (x1 + x2).abs()
+        bnd[0][lo:hi] = edg @ W[0].abs().T + edu @ W[1].abs().T + 2 * (4 * p + 1) * u * (a1 + a2) + r_ * (x1 + x2).abs()
         for i, (l, v, el, ev) in enumerate([(xe, dg, None, edg), (xe, du, None, edu), (h, d, eh, None)]):
             o, mag = _mm(l.T, v)
-            b = 2 * (n + 1) * u * mag + r_ * o.abs()
+            b = 2 * (2 * n + 1) * u * mag + r_ * o.abs()
             b += l.abs().T @ ev if ev is not None else el.T @ v.abs()
             out[i + 1][e], bnd[i + 1][e] = o, b
     return out, bnd
