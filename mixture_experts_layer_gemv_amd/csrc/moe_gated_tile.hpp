@@ -219,8 +219,7 @@ struct Vec {
 };
 
 template <class T>
-__device__ __forceinline__ Vec<T> load_vec(const void* p, size_t i) {
-  const u32x4_t r = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + i * T::ES);
+__device__ __forceinline__ Vec<T> to_vec(u32x4_t r) {
   Vec<T> f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -272,14 +271,23 @@ __device__ __forceinline__ float sigmoid(float g) {
   else return 1.0f / (1.0f + expf(-g));
 }
 
+// How a wave takes the 32 rows of a block of 32 CH channels, 16 bytes of outputs a
+// lane: in pass q of PASSES a lane has row q RPI + lane / LPR, channel N (lane % LPR).
+template <class T, int CH>
+struct RowWalk {
+  static constexpr int N = Vec<T>::N, LPR = 32 * CH / N, RPI = 64 / LPR, PASSES = 32 / RPI;
+  static __device__ __forceinline__ int row(int q, int lane) { return q * RPI + lane / LPR; }
+  static __device__ __forceinline__ int channel(int lane) { return lane % LPR * N; }
+};
+
 // Hands out the accumulators of row block i as rows: a wave stages 32 rows of its
-// 32 CB channels in LDS as fp32 (rows padded by 16 bytes) and f(row, channel,
+// 32 CB channels in LDS as fp32 (rows padded by 16 bytes) and f(pass, row, channel,
 // values) gets Vec<T>::N channels at `channel` of the first 32 CH and, where CH
 // is less than CB, the same of the second.
 template <class T, int TB, int CB, int CH, class F>
 __device__ __forceinline__ void each_vec(const f32x16_t (&acc)[CB][TB], int i, unsigned char* stage, int lane, F f) {
+  using Walk = RowWalk<T, CH>;
   constexpr int STR = 32 * CB * 4 + 16, N = Vec<T>::N;
-  constexpr int LPR = 32 * CH / N, RPI = 64 / LPR;  // lanes per row, rows a pass
   unsigned char* const mine = stage + (lane & 31) * STR + 16 * (lane >> 5);
 #pragma unroll
   for (int c = 0; c < CB; ++c)
@@ -291,8 +299,8 @@ __device__ __forceinline__ void each_vec(const f32x16_t (&acc)[CB][TB], int i, u
   // place in order; the compiler must keep them so across the types)
   asm volatile("" ::: "memory");
 #pragma unroll
-  for (int q = 0; q < 32 / RPI; ++q) {
-    const int r = q * RPI + lane / LPR, ch = lane % LPR * N;
+  for (int q = 0; q < Walk::PASSES; ++q) {
+    const int r = Walk::row(q, lane), ch = Walk::channel(lane);
     Vec<T> a, b;
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
@@ -305,7 +313,7 @@ __device__ __forceinline__ void each_vec(const f32x16_t (&acc)[CB][TB], int i, u
         for (int v = 0; v < 4; ++v) b.v[j + v] = hi[v];
       }
     }
-    f(r, ch, a, b);
+    f(q, r, ch, a, b);
   }
   asm volatile("" ::: "memory");
 }
@@ -327,9 +335,22 @@ __device__ __forceinline__ int2 expert_rows(const int32_t* offsets, int E, int R
 
 // ---- products over the experts' rows --------------------------------------------
 
+// What an output's element `at` takes from memory besides its sums: gate and up for
+// the hidden gradients.
+struct Saved {
+  u32x4_t gate, up;
+};
+template <Op OP, int ES>
+__device__ __forceinline__ Saved load_saved(const GatedArgs& A, size_t at) {
+  if constexpr (OP == Op::kGradHidden)
+    return {*reinterpret_cast<const u32x4_t*>(static_cast<const char*>(A.in[0]) + at * ES),
+            *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(A.in[1]) + at * ES)};
+  else return {};
+}
+
 // The outputs at element `at` from its sums (gated: a gate's, b up's).
 template <class T, Op OP>
-__device__ __forceinline__ void finish(const GatedArgs& A, size_t at, const Vec<T>& a, const Vec<T>& b) {
+__device__ __forceinline__ void finish(const GatedArgs& A, size_t at, const Vec<T>& a, const Vec<T>& b, const Saved& saved) {
   constexpr int V = Vec<T>::N;
   if constexpr (OP == Op::kUp) {
     Vec<T> h;
@@ -340,7 +361,7 @@ __device__ __forceinline__ void finish(const GatedArgs& A, size_t at, const Vec<
     if (A.out[2]) store_vec<T>(A.out[2], at, b);
   } else if constexpr (OP == Op::kGradHidden) {
     // h = g s u with s = sigmoid(g): dg = dh u s (1 + g (1 - s)), du = dh g s
-    const Vec<T> g = load_vec<T>(A.in[0], at), u = load_vec<T>(A.in[1], at);
+    const Vec<T> g = to_vec<T>(saved.gate), u = to_vec<T>(saved.up);
     Vec<T> dg, du, h;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -391,7 +412,8 @@ __global__ __launch_bounds__(256) void k_gated_join(const GatedArgs A, int split
           for (int v = 0; v < 4; ++v) b.v[j + v] += g[v];
         }
       }
-    finish<T, OP>(A, (size_t)r * A.N + c, a, b);
+    const size_t at = (size_t)r * A.N + c;
+    finish<T, OP>(A, at, a, b, load_saved<OP, T::ES>(A, at));
   }
 }
 
@@ -503,24 +525,38 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
   constexpr int CH = GATED ? CB / 2 : CB;
   unsigned char* const stage = ring + wave * 32 * (32 * CB * 4 + 16);
   const int nw = n0 + 32 * CH * wc;  // the wave's first output column
+  // gate and up are loaded a row block ahead (hidden gradients of 16384 rows, 4096 x
+  // 6400: 955 us with a wait in each pass, so 947)
+  using Walk = RowWalk<T, CH>;
+  Saved saved[2][Walk::PASSES];
+  auto fetch = [&](int i) {
+    if (OP != Op::kGradHidden || splits > 1) return;
+#pragma unroll
+    for (int q = 0; q < Walk::PASSES; ++q) {
+      const int r = min((wt * TB + i) * 32 + Walk::row(q, lane), rows - 1), c = min(nw + Walk::channel(lane), N - Vec<T>::N);
+      saved[i & 1][q] = load_saved<OP, T::ES>(A, (size_t)(row0 + r) * N + c);
+    }
+  };
+  fetch(0);
 #pragma unroll
   for (int i = 0; i < TB; ++i) {
     const int rb = (wt * TB + i) * 32;
     if (rb >= rows) break;
+    if (i + 1 < TB) fetch(i + 1);
     if (splits > 1) {  // fp32 partial sums, a row's gate and then its up
       const int lines = GATED ? 2 * N : N;
       float* const part = A.part + ((size_t)split * A.R + row0) * lines;
-      each_vec<F32, TB, CB, CB>(acc, i, stage, lane, [&](int r, int ch, const Vec<F32>& a, const Vec<F32>&) {
+      each_vec<F32, TB, CB, CB>(acc, i, stage, lane, [&](int, int r, int ch, const Vec<F32>& a, const Vec<F32>&) {
         const int col = nw + (GATED ? ch % (32 * CH) : ch);
         if (rb + r < rows && col < N)
           store_vec<F32>(part, (size_t)(rb + r) * lines + col + (GATED && ch >= 32 * CH ? N : 0), a);
       });
       continue;
     }
-    each_vec<T, TB, CB, CH>(acc, i, stage, lane, [&](int r, int ch, const Vec<T>& a, const Vec<T>& b) {
+    each_vec<T, TB, CB, CH>(acc, i, stage, lane, [&](int q, int r, int ch, const Vec<T>& a, const Vec<T>& b) {
       if (rb + r >= rows || nw + ch >= N) return;
       const size_t at = (size_t)(row0 + rb + r) * N + nw + ch;
-      finish<T, OP>(A, at, a, b);
+      finish<T, OP>(A, at, a, b, saved[i & 1][q]);
     });
   }
 }
@@ -612,7 +648,7 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
   for (int i = 0; i < TB; ++i) {
     const int rb = m0 + (wt * TB + i) * 32;
     if (rb >= M) break;
-    each_vec<T, TB, CB, CB>(acc, i, stage, lane, [&](int r, int ch, const Vec<T>& a, const Vec<T>&) {
+    each_vec<T, TB, CB, CB>(acc, i, stage, lane, [&](int, int r, int ch, const Vec<T>& a, const Vec<T>&) {
       if (rb + r < M && nw + ch < N) store_vec<T>(P.out, out0 + (size_t)(rb + r) * N + nw + ch, a);
     });
   }
