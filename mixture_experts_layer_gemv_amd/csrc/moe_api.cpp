@@ -1921,8 +1921,9 @@ GatedSpace gated_space(int dtype, int rows, int m, int p, int E, bool backward) 
   s.hidden = align256((size_t)rows * p * es);
   s.rows = align256((size_t)rows * m * es);
   s.low = moe::gated_low_parts(bf16, rows, E);
-  s.part = backward ? std::max(moe::gated_part_bytes(bf16, false, rows, m, p, E, 1, cus),
-                               moe::gated_part_bytes(bf16, false, rows, p, m, E, 2, cus))
+  s.part = backward ? std::max({moe::gated_part_bytes(bf16, false, rows, m, p, E, 1, cus),
+                                moe::gated_part_bytes(bf16, false, rows, p, m, E, 2, cus),
+                                moe::grad_w_part_bytes(bf16, rows, m, p, E, cus)})
                     : std::max(moe::gated_part_bytes(bf16, true, rows, m, p, E, 1, cus),
                                moe::gated_part_bytes(bf16, false, rows, p, m, E, 1, cus));
   return s;
@@ -2135,11 +2136,14 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
     w.offsets = offsets;
     w.R = rows;
     w.E = E;
+    w.m = m;
+    w.p = p;
+    w.part = part;
     if (dw_gate) {
-      w.p[w.n++] = {xr, dg, low ? xr : nullptr, low ? dg + low : nullptr, dw_gate, m, p};
-      w.p[w.n++] = {xr, du, low ? xr : nullptr, low ? du + low : nullptr, dw_up, m, p};
+      w.problem[w.n++] = {xr, dg, low ? xr : nullptr, low ? dg + low : nullptr, dw_gate, m, p};
+      w.problem[w.n++] = {xr, du, low ? xr : nullptr, low ? du + low : nullptr, dw_up, m, p};
     }
-    if (dw_down) w.p[w.n++] = {h, dy_perm, low ? h + low : nullptr, low ? dy_perm : nullptr, dw_down, p, m};
+    if (dw_down) w.problem[w.n++] = {h, dy_perm, low ? h + low : nullptr, low ? dy_perm : nullptr, dw_down, p, m};
     MOE_TRY_HIP(run("gated_grad_w", s, [&] { return moe::launch_gated_grad_w(w, bf16, device_cus(), s); }));
   }
   if (dx_perm && rows > 0) {

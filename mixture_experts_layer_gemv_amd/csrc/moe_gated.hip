@@ -44,6 +44,11 @@ size_t gated_part_bytes(bool bf16, bool gated, int R, int K, int N, int E, int t
   return c.splits > 1 ? (size_t)c.splits * R * lines * sizeof(float) : 0;
 }
 
+size_t grad_w_part_bytes(bool bf16, int R, int m, int p, int E, int cus) {
+  const GradWChoice c = choose_grad_w(bf16, R, m, p, E, cus);
+  return c.splits > 1 ? (size_t)c.splits * 3 * E * m * p * sizeof(float) : 0;
+}
+
 hipError_t gated_up_bf16(const GatedArgs& a, int cus, hipStream_t s);
 hipError_t gated_up_f32(const GatedArgs& a, int cus, hipStream_t s);
 hipError_t gated_down_bf16(const GatedArgs& a, int cus, hipStream_t s);
@@ -86,7 +91,7 @@ hipError_t launch_gated_grad_w(const GradWArgs& a, bool bf16, int cus, hipStream
   if (a.n <= 0) return hipSuccess;
   if (a.n > 3 || a.R < 0 || a.E < 1 || a.E > 64 || (!a.offsets && a.E != 1)) return hipErrorInvalidValue;
   for (int i = 0; i < a.n; ++i)
-    if (a.p[i].M <= 0 || a.p[i].M % 8 || a.p[i].M > kGatedMaxCols || a.p[i].N <= 0 || a.p[i].N % 8 || a.p[i].N > kGatedMaxCols)
+    if (a.problem[i].M <= 0 || a.problem[i].M % 8 || a.problem[i].M > kGatedMaxCols || a.problem[i].N <= 0 || a.problem[i].N % 8 || a.problem[i].N > kGatedMaxCols)
       return hipErrorInvalidValue;
   return bf16 ? gated_grad_w_bf16(a, cus, s) : gated_grad_w_f32(a, cus, s);
 }

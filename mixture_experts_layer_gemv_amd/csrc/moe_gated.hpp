@@ -42,11 +42,13 @@ struct GradWProblem {
   int M, N;
 };
 struct GradWArgs {
-  GradWProblem p[3];
+  GradWProblem problem[3];
   int n;  // problems
   const int32_t* offsets;
-  int R, E;
+  int R, E, m, p;  // m, p: of the block, whatever problems there are
+  float* part;     // workspace of split reductions (grad_w_part_bytes), or null: none is split
 };
+size_t grad_w_part_bytes(bool bf16, int R, int m, int p, int E, int cus);
 
 // bf16 or fp32 operands and outputs, fp32 sums.
 //   gated_up:    out[0] = silu(x w0) * (x w1); out[1], out[2] = x w0, x w1 (or null)   w [E][K][N]

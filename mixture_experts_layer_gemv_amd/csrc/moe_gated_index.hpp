@@ -121,11 +121,16 @@ inline GatedChoice choose_gated(bool bf16, int R, long long lines, int stages, i
     else tile = kGated32x256x3, n = items(32, 256);
   } else {
     // fp32's products take eight times as long, so it is their count that matters,
-    // rows past an expert's last among it: 4096 x 2048 x 8192: 1.01 ms (139 TFLOP/s), 64 x 128 1.10
-    if (avg > 512) tile = kGated128x128x2, n = items(128, 128), slots = 2 * cus;
-    // 207 rows each of 5, 1000 x 712: hidden gradients 35, 128 x 128 47 us (both split)
-    else if (avg > 112) tile = kGated64x128x3, n = items(64, 128), slots = 2 * cus;
-    // 83 rows each of 12, 1000 x 1720: gate and up 82, 128 x 128 131, 64 x 128 118 us
+    // rows past an expert's last among it: 83 rows each of 12, 1000 x 1720: gate and up
+    // 82, 128 x 128 131, 64 x 128 118 us; and every CU needs a share of them.
+    auto fills = [&](int BM) {
+      const long long tiles = items(BM, 128), most = 2 * cus / tiles, shares = most < stages / 4 ? most : stages / 4;
+      return 4 * tiles * (shares > 1 ? shares : 1) >= 6 * cus;
+    };
+    // 4096 x 2048 x 8192: 1.01 ms (139 TFLOP/s), 64 x 128 1.10
+    if (avg > 512 && fills(128)) tile = kGated128x128x2, n = items(128, 128), slots = 2 * cus;
+    // 207 rows each of 5, 1000 x 712: hidden gradients 35, 128 x 128 47, 32 x 128 41 us (all split)
+    else if (avg > 112 && fills(64)) tile = kGated64x128x3, n = items(64, 128), slots = 2 * cus;
     else tile = kGated32x128x2, n = items(32, 128), slots = 4 * cus;
   }
   // Too few tiles to fill the CUs share their reductions, at least four stages each:
@@ -138,6 +143,24 @@ inline GatedChoice choose_gated(bool bf16, int R, long long lines, int stages, i
   // Small ones, warm: 17.8 -> 21.4 us (1024 x 2048).
   const bool once = bf16 && avg <= 32 && (long long)experts * lines * stages * 128 >= 128LL << 20;
   return {tile, splits < 2 ? 1 : (int)splits, once};
+}
+
+// The weight gradients of R rows of E experts (two of m x p, one of p x m): 256 x 256
+// tiles, or else 128 x 128, and the number of blocks that share a tile's rows.
+struct GradWChoice {
+  bool wide;
+  int splits;
+};
+inline GradWChoice choose_grad_w(bool bf16, int R, int m, int p, int E, int cus) {
+  auto tiles = [&](int B) { return 3LL * E * ((m + B - 1) / B) * ((p + B - 1) / B); };
+  // 16 experts, 4096 x 6400: 2.4 ms with 256 x 256 tiles.  Fewer than two a CU are halved:
+  // 207 rows each of 5, 1000 x 712 in fp32: 85 -> 62 us
+  if (bf16 && tiles(256) >= 2 * cus) return {true, 1};
+  const int steps = stage_steps(bf16 ? 2 : 4);
+  const long long stages = (R / E + steps - 1) / steps;
+  long long splits = 2 * cus / tiles(128);
+  if (splits > stages / 4) splits = stages / 4;
+  return {false, splits < 2 ? 1 : splits > 32 ? 32 : (int)splits};  // XX
 }
 
 }  // namespace moe

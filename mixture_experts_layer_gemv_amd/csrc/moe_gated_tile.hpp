@@ -98,6 +98,13 @@ __device__ __forceinline__ Stages stages_of(int K, int KD, int terms) {
   return {0, per * terms, per, left != KD, (left + KD / 4 - 1) / (KD / 4)};
 }
 
+__device__ __forceinline__ Stages share_of(Stages st, int split, int splits) {
+  const int all = st.hi;
+  st.lo = (int)((long long)all * split / splits);
+  st.hi = (int)((long long)all * (split + 1) / splits);
+  return st;
+}
+
 // The products of a workgroup's stages into acc.  at(s) is what the copies of stage
 // s start from; issue(at, slot, j, partial) makes copy j of the wave's Sh::CP.
 // live: the wave's row blocks that hold rows (an expert's last tile); the others are
@@ -465,11 +472,7 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
   }
   const uint32_t lds0 = lds_address(&ring[0]);
   Stages st = stages_of(K, KD, TWO ? 2 : 1);
-  if (splits > 1) {
-    const int all = st.hi;
-    st.lo = (int)((long long)all * split / splits);
-    st.hi = (int)((long long)all * (split + 1) / splits);
-  }
+  if (splits > 1) st = share_of(st, split, splits);
   const size_t wstart = ((size_t)it.e * N * K + (WS ? 0 : (size_t)n0 * K)) * ES;
   const char* const w0 = static_cast<const char*>(A.w[0]) + wstart;
   const char* const w1 = GATED || TWO ? static_cast<const char*>(A.w[1]) + wstart : nullptr;
@@ -525,24 +528,11 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
   constexpr int CH = GATED ? CB / 2 : CB;
   unsigned char* const stage = ring + wave * 32 * (32 * CB * 4 + 16);
   const int nw = n0 + 32 * CH * wc;  // the wave's first output column
-  // gate and up are loaded a row block ahead (hidden gradients of 16384 rows, 4096 x
-  // 6400: 955 us with a wait in each pass, so 947)
   using Walk = RowWalk<T, CH>;
-  Saved saved[2][Walk::PASSES];
-  auto fetch = [&](int i) {
-    if (OP != Op::kGradHidden || splits > 1) return;
-#pragma unroll
-    for (int q = 0; q < Walk::PASSES; ++q) {
-      const int r = min((wt * TB + i) * 32 + Walk::row(q, lane), rows - 1), c = min(nw + Walk::channel(lane), N - Vec<T>::N);
-      saved[i & 1][q] = load_saved<OP, T::ES>(A, (size_t)(row0 + r) * N + c);
-    }
-  };
-  fetch(0);
 #pragma unroll
   for (int i = 0; i < TB; ++i) {
     const int rb = (wt * TB + i) * 32;
     if (rb >= rows) break;
-    if (i + 1 < TB) fetch(i + 1);
     if (splits > 1) {  // fp32 partial sums, a row's gate and then its up
       const int lines = GATED ? 2 * N : N;
       float* const part = A.part + ((size_t)split * A.R + row0) * lines;
@@ -553,10 +543,19 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
       });
       continue;
     }
+    // gate and up of the whole row block are loaded together (hidden gradients of 16384
+    // rows, 4096 x 6400: 955 us with a wait in each pass, so 948)
+    Saved saved[Walk::PASSES] = {};
+    if constexpr (OP == Op::kGradHidden)
+#pragma unroll
+      for (int q = 0; q < Walk::PASSES; ++q) {
+        const int r = min(rb + Walk::row(q, lane), rows - 1), c = min(nw + Walk::channel(lane), N - Vec<T>::N);
+        saved[q] = load_saved<OP, T::ES>(A, (size_t)(row0 + r) * N + c);
+      }
     each_vec<T, TB, CB, CH>(acc, i, stage, lane, [&](int q, int r, int ch, const Vec<T>& a, const Vec<T>& b) {
       if (rb + r >= rows || nw + ch >= N) return;
       const size_t at = (size_t)(row0 + rb + r) * N + nw + ch;
-      finish<T, OP>(A, at, a, b, saved[i & 1][q]);
+      finish<T, OP>(A, at, a, b, saved[q]);
     });
   }
 }
@@ -567,7 +566,7 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
 template <class T, int TB, int CB, int WT, int WC, int S, bool PAIR>
 __global__ __launch_bounds__(WT* WC * 64)
     __attribute__((amdgpu_waves_per_eu(TileShape<TB, CB, WT, WC, S>::per_simd, TileShape<TB, CB, WT, WC, S>::per_simd)))
-void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
+void k_gated_grad_w(const GradWArgs A, int cg, int per_expert, int splits) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
   constexpr int ES = T::ES, KD = stage_steps(ES);
   __shared__ __attribute__((aligned(1024))) unsigned char ring[S * (Sh::XB + Sh::WB)];
@@ -575,17 +574,18 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WC, wc = wave % WC;
   // the item: expert, problem, tile
-  const ExpertItem it = expert_item((int)blockIdx.x, per_expert);
+  const int items = (int)gridDim.x / splits, split = (int)blockIdx.x / items;
+  const ExpertItem it = expert_item((int)blockIdx.x - split * items, per_expert);
   const int e = it.e;
   if (e >= A.E) return;
   int li = it.tile, q = 0, MB = 0, NB = 0;
   for (;; ++q) {
-    MB = (A.p[q].M + Sh::BM - 1) / Sh::BM;
-    NB = (A.p[q].N + Sh::BN - 1) / Sh::BN;
+    MB = (A.problem[q].M + Sh::BM - 1) / Sh::BM;
+    NB = (A.problem[q].N + Sh::BN - 1) / Sh::BN;
     if (li < MB * NB || q + 1 >= A.n) break;
     li -= MB * NB;
   }
-  const GradWProblem P = A.p[q];
+  const GradWProblem P = A.problem[q];
   const int M = P.M, N = P.N;
   const int g = li / (MB * cg), rem = li - g * MB * cg, gw = min(NB - g * cg, cg);
   const int m0 = rem / gw * Sh::BM, n0 = (g * cg + rem % gw) * Sh::BN;
@@ -606,7 +606,8 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
               (uint32_t)line_step(i, ES) * (uint32_t)(N * ES);
   }
   const uint32_t lds0 = lds_address(&ring[0]);
-  const Stages st = stages_of(K, KD, PAIR ? 2 : 1);
+  Stages st = stages_of(K, KD, PAIR ? 2 : 1);
+  if (splits > 1) st = share_of(st, split, splits);
   const char* const x0 = static_cast<const char*>(P.x) + (size_t)lo * M * ES;
   const char* const w0 = static_cast<const char*>(P.w) + (size_t)lo * N * ES;
   const char* const x1 = PAIR ? static_cast<const char*>(P.x2) + (size_t)lo * M * ES : nullptr;
@@ -648,9 +649,36 @@ void k_gated_grad_w(const GradWArgs A, int cg, int per_expert) {
   for (int i = 0; i < TB; ++i) {
     const int rb = m0 + (wt * TB + i) * 32;
     if (rb >= M) break;
+    if (splits > 1) {  // fp32 partial sums [problem][split][E][M][N]
+      float* const part = A.part + ((size_t)q * splits + split) * A.E * M * N;
+      each_vec<F32, TB, CB, CB>(acc, i, stage, lane, [&](int, int r, int ch, const Vec<F32>& a, const Vec<F32>&) {
+        if (rb + r < M && nw + ch < N) store_vec<F32>(part, out0 + (size_t)(rb + r) * N + nw + ch, a);
+      });
+      continue;
+    }
     each_vec<T, TB, CB, CB>(acc, i, stage, lane, [&](int, int r, int ch, const Vec<T>& a, const Vec<T>&) {
       if (rb + r < M && nw + ch < N) store_vec<T>(P.out, out0 + (size_t)(rb + r) * N + nw + ch, a);
     });
+  }
+}
+
+// Joins split weight gradients: blockIdx.y is the problem.
+template <class T>
+__global__ __launch_bounds__(256) void k_grad_w_join(const GradWArgs A, int splits) {
+  constexpr int V = Vec<T>::N;
+  const size_t n = (size_t)A.E * A.m * A.p;
+  const float* const part = A.part + (size_t)blockIdx.y * splits * n;
+  void* const out = A.problem[blockIdx.y].out;
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * V; i < n; i += (size_t)gridDim.x * 256 * V) {
+    Vec<T> a = {};
+    for (int k = 0; k < splits; ++k)
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const f32x4_t f = *reinterpret_cast<const f32x4_t*>(part + k * n + i + j);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a.v[j + v] += f[v];
+      }
+    store_vec<T>(out, i, a);
   }
 }
 
@@ -676,7 +704,7 @@ hipError_t launch_tile(const GatedArgs& a, int cg, int splits, hipStream_t s) {
 // The product with the tile that choose_gated names.
 template <class T, Op OP>
 hipError_t rows_product(const GatedArgs& a, int cus, hipStream_t s) {
-  constexpr int cg = 4;  // column blocks that share their rows in an XCD's L2
+  constexpr int cg = 4;  // column blocks that share their rows in an XCD's L2 (2: the same, 8: 2 %, 16: 7 % slower)
   constexpr int KD = stage_steps(T::ES);
   const GatedChoice c = choose_gated(T::ES == 2, a.R, OP == Op::kUp ? 2LL * a.N : a.N,
                                      (a.K + KD - 1) / KD * (OP == Op::kGradX ? 2 : 1), a.E, cus);
@@ -706,33 +734,34 @@ hipError_t rows_product(const GatedArgs& a, int cus, hipStream_t s) {
   }
 }
 
-inline long long grad_w_tiles(const GradWArgs& a, int BM, int BN) {
-  long long per = 0;
-  for (int i = 0; i < a.n; ++i) per += (long long)((a.p[i].M + BM - 1) / BM) * ((a.p[i].N + BN - 1) / BN);
-  return per;
-}
-
 template <class T, int TB, int CB, int WT, int WC, int S, bool PAIR>
-hipError_t launch_grad_w_tile(const GradWArgs& a, int cg, hipStream_t s) {
+hipError_t launch_grad_w_tile(const GradWArgs& a, int cg, int splits, hipStream_t s) {
   using Sh = TileShape<TB, CB, WT, WC, S>;
-  const long long per = grad_w_tiles(a, Sh::BM, Sh::BN);
-  const long long blocks = (per + 7) / 8 * 8 * a.E;
+  long long per = 0;
+  for (int i = 0; i < a.n; ++i)
+    per += (long long)((a.problem[i].M + Sh::BM - 1) / Sh::BM) * ((a.problem[i].N + Sh::BN - 1) / Sh::BN);
+  const long long blocks = (per + 7) / 8 * 8 * a.E * splits;
   if (blocks * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
-  k_gated_grad_w<T, TB, CB, WT, WC, S, PAIR><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, (int)per);
+  k_gated_grad_w<T, TB, CB, WT, WC, S, PAIR><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, (int)per, splits);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || splits == 1) return e;
+  const long long vecs = (long long)a.E * a.m * a.p / Vec<T>::N, n = (vecs + 255) / 256;
+  k_grad_w_join<T><<<dim3((unsigned)(n < 1 << 20 ? n : 1 << 20), a.n), 256, 0, s>>>(a, splits);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t grad_w_product(const GradWArgs& a, int cus, hipStream_t s) {
-  constexpr int cg = 4;
+  constexpr int cg = 4;  // column blocks that share their rows in an XCD's L2 (2 to 8: within 1 %)
+  const GradWChoice c = choose_grad_w(T::ES == 2, a.R, a.m, a.p, a.E, cus);
+  if (c.splits > 1 && !a.part) return hipErrorInvalidValue;
   if constexpr (T::ES == 2) {
     bool pair = true;
-    for (int i = 0; i < a.n; ++i) pair = pair && a.p[i].x2 && a.p[i].w2;
-    if (grad_w_tiles(a, 256, 256) * a.E >= 2 * cus)
-      return pair ? launch_grad_w_tile<T, 4, 2, 2, 4, 2, true>(a, cg, s) : launch_grad_w_tile<T, 4, 2, 2, 4, 2, false>(a, cg, s);
-    if (pair) return launch_grad_w_tile<T, 2, 2, 2, 2, 2, true>(a, cg, s);
+    for (int i = 0; i < a.n; ++i) pair = pair && a.problem[i].x2 && a.problem[i].w2;
+    if (c.wide)
+      return pair ? launch_grad_w_tile<T, 4, 2, 2, 4, 2, true>(a, cg, 1, s) : launch_grad_w_tile<T, 4, 2, 2, 4, 2, false>(a, cg, 1, s);
+    if (pair) return launch_grad_w_tile<T, 2, 2, 2, 2, 2, true>(a, cg, c.splits, s);
   }
-  return launch_grad_w_tile<T, 2, 2, 2, 2, 2, false>(a, cg, s);
+  return launch_grad_w_tile<T, 2, 2, 2, 2, 2, false>(a, cg, c.splits, s);
 }
 
 }  // namespace
