@@ -430,7 +430,7 @@ template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE, bool
 __global__ __launch_bounds__(WT* WC * 64)
     __attribute__((amdgpu_waves_per_eu(RowsShape<TB, CB, WT, WC, S, PAIR>::per_simd,
                                        RowsShape<TB, CB, WT, WC, S, PAIR>::per_simd)))
-void k_gated_rows(const GatedArgs A, int cg, int splits) {
+void k_gated_rows(const GatedArgs A, int cg, int splits, int cut) {
   using Sh = RowsShape<TB, CB, WT, WC, S, PAIR>;
   static_assert(!PAIR || (TB == 1 && WT == 1), "the pair's lines follow one another");
   constexpr int BM = 32 * TB * WT;  // rows of a tile
@@ -444,7 +444,7 @@ void k_gated_rows(const GatedArgs A, int cg, int splits) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WC, wc = wave % WC;
   const int items = (int)gridDim.x / splits, split = (int)blockIdx.x / items;
-  const Item it = find_item(A.offsets, A.E, A.R, BM, (A.N + BN - 1) / BN, cg, (int)blockIdx.x - split * items, true);
+  const Item it = find_item(A.offsets, A.E, A.R, BM, (A.N + BN - 1) / BN, cg, (int)blockIdx.x - split * items, true, BM == 256 ? cut : 0);
   if (it.e < 0) return;
   const int row0 = it.row0, rows = it.rows, n0 = it.nb * BN;
 
@@ -690,11 +690,13 @@ inline long long row_blocks(const GatedArgs& a, int BM) {
 }
 
 template <class T, Op OP, int TB, int CB, int WT, int WC, int S, bool ONCE = false, bool PAIR = false>
-hipError_t launch_tile(const GatedArgs& a, int cg, int splits, hipStream_t s) {
+hipError_t launch_tile(const GatedArgs& a, int cg, int splits, int cus, hipStream_t s) {
   constexpr int BM = 32 * TB * WT, BN = 32 * CB * WC / (OP == Op::kUp ? 2 : 1);
-  const long long blocks = (row_blocks(a, BM) * ((a.N + BN - 1) / BN) + 7) / 8 * 8 * splits;
+  const long long most = row_blocks(a, BM) * ((a.N + BN - 1) / BN);
+  const int cut = BM == 256 && splits == 1 ? cus : 0;
+  const long long blocks = cut ? cut_blocks(most, cut) : (most + 7) / 8 * 8 * splits;
   if (blocks * WT * WC * 64 >= 1LL << 32) return hipErrorInvalidValue;
-  k_gated_rows<T, OP, TB, CB, WT, WC, S, ONCE, PAIR><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, splits);
+  k_gated_rows<T, OP, TB, CB, WT, WC, S, ONCE, PAIR><<<(unsigned)blocks, WT * WC * 64, 0, s>>>(a, cg, splits, cut);
   if (hipError_t e = hipGetLastError(); e != hipSuccess || splits == 1) return e;
   const long long vecs = (long long)a.R * (a.N / Vec<T>::N), n = (vecs + 255) / 256;
   k_gated_join<T, OP><<<(unsigned)(n < 1 << 20 ? n : 1 << 20), 256, 0, s>>>(a, splits);
@@ -713,23 +715,23 @@ hipError_t rows_product(const GatedArgs& a, int cus, hipStream_t s) {
   if (T::ES == 2 && (gated_pairs(true, a.R, a.E) != (a.low != 0))) return hipErrorInvalidValue;
   if constexpr (T::ES == 2) {
     switch (c.tile) {
-      case kGated256x256x2: return launch_tile<T, OP, 4, 2, 2, 4, 2>(a, cg, c.splits, s);
-      case kGated128x256x3: return launch_tile<T, OP, 2, 2, 2, 4, 3>(a, cg, c.splits, s);
-      case kGated128x128x2: return launch_tile<T, OP, 2, 2, 2, 2, 2>(a, cg, c.splits, s);
-      case kGated64x128x3: return launch_tile<T, OP, 1, 2, 2, 2, 3>(a, cg, c.splits, s);
+      case kGated256x256x2: return launch_tile<T, OP, 4, 2, 2, 4, 2>(a, cg, c.splits, cus, s);
+      case kGated128x256x3: return launch_tile<T, OP, 2, 2, 2, 4, 3>(a, cg, c.splits, cus, s);
+      case kGated128x128x2: return launch_tile<T, OP, 2, 2, 2, 2, 2>(a, cg, c.splits, cus, s);
+      case kGated64x128x3: return launch_tile<T, OP, 1, 2, 2, 2, 3>(a, cg, c.splits, cus, s);
       case kGated32x256x2:
-        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 2, true, PAIR>(a, cg, c.splits, s)
-                      : launch_tile<T, OP, 1, 2, 1, 4, 2, false, PAIR>(a, cg, c.splits, s);
+        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 2, true, PAIR>(a, cg, c.splits, cus, s)
+                      : launch_tile<T, OP, 1, 2, 1, 4, 2, false, PAIR>(a, cg, c.splits, cus, s);
       case kGated32x256x3:
-        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 3, true, PAIR>(a, cg, c.splits, s)
-                      : launch_tile<T, OP, 1, 2, 1, 4, 3, false, PAIR>(a, cg, c.splits, s);
+        return c.once ? launch_tile<T, OP, 1, 2, 1, 4, 3, true, PAIR>(a, cg, c.splits, cus, s)
+                      : launch_tile<T, OP, 1, 2, 1, 4, 3, false, PAIR>(a, cg, c.splits, cus, s);
       default: return hipErrorInvalidValue;
     }
   }
   switch (c.tile) {
-    case kGated128x128x2: return launch_tile<T, OP, 2, 2, 2, 2, 2>(a, cg, c.splits, s);
-    case kGated64x128x3: return launch_tile<T, OP, 1, 2, 2, 2, 3>(a, cg, c.splits, s);
-    case kGated32x128x2: return launch_tile<T, OP, 1, 2, 1, 2, 2>(a, cg, c.splits, s);
+    case kGated128x128x2: return launch_tile<T, OP, 2, 2, 2, 2, 2>(a, cg, c.splits, cus, s);
+    case kGated64x128x3: return launch_tile<T, OP, 1, 2, 2, 2, 3>(a, cg, c.splits, cus, s);
+    case kGated32x128x2: return launch_tile<T, OP, 1, 2, 1, 2, 2>(a, cg, c.splits, cus, s);
     default: return hipErrorInvalidValue;
   }
 }

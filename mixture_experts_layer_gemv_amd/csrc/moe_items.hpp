@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "moe_gated_index.hpp"
 #include "moe_index.hpp"
 
 namespace moe {
@@ -22,13 +23,27 @@ struct Item {
 // offsets are clamped to [0, R], a decreasing entry counting as its
 // predecessor, so that the ranges are disjoint and in bounds whatever the
 // caller's array holds.  spread: L is the block's number, dealt evenly over
-// the XCDs (xcd_item); else it is the item.
-__device__ __forceinline__ Item find_item(const int32_t* offsets, int E, int R, int BM, int NBL, int cg, int L, bool spread) {
+// the XCDs (xcd_item); else it is the item.  cut: see cut_last_round; the grid then
+// has to hold cut_blocks blocks.
+__device__ __forceinline__ Item find_item(const int32_t* offsets, int E, int R, int BM, int NBL, int cg, int L, bool spread,
+                                          int cut = 0) {
   Item it{-1, 0, 0, 0, 0, 0};
+  int half = -1;
+  auto item_of = [&](int b, int total) {
+    if (!spread) return b;
+    const int last = cut ? cut_last_round(total, cut) : 0;
+    if (!last) return xcd_item(b, total, 0);
+    int i = xcd_item(b, total - last, 2 * last);
+    if (i >= total - last) {
+      half = (i - (total - last)) & 1;
+      i = total - last + ((i - (total - last)) >> 1);
+    }
+    return i;
+  };
   int e = 0, lo = 0, hi = R, before = 0;  // the item's expert, its rows, the items before it
   if (!offsets) {
     const int total = (hi + BM - 1) / BM * NBL;
-    if (spread) L = xcd_item(L, total, 0);
+    L = item_of(L, total);
     if (L < 0 || L >= total) return it;
   } else {
     const int lane = threadIdx.x & 63;
@@ -49,7 +64,7 @@ __device__ __forceinline__ Item find_item(const int32_t* offsets, int E, int R, 
       if (lane >= d) sum += p;
     }
     const int total = __builtin_amdgcn_readlane(sum, 63);
-    if (spread) L = xcd_item(L, total, 0);
+    L = item_of(L, total);
     if (L < 0 || L >= total) return it;
     e = __builtin_ctzll(__ballot(L < sum));
     before = __builtin_amdgcn_readlane(sum - items, e);
@@ -70,6 +85,11 @@ __device__ __forceinline__ Item find_item(const int32_t* offsets, int E, int R, 
   it.blocks = blocks;
   it.row0 = lo + it.mb * BM;
   it.rows = min(BM, hi - it.row0);
+  if (half >= 0) {
+    it.row0 += half * (BM / 2);
+    it.rows = half ? it.rows - BM / 2 : min(it.rows, BM / 2);
+    if (it.rows <= 0) it.e = -1;
+  }
   return it;
 }
 

@@ -118,7 +118,29 @@ static void items(int E, int tiles) {
   CHECK((int)seen.size() == E * tiles, "%zu of %d x %d", seen.size(), E, tiles);
 }
 
+// Items of which the last round's are cut in two: each whole item once, each half once,
+// within the blocks that the launch holds.
+static void cut(int most, int total, int cus) {
+  const int last = moe::cut_last_round(total, cus);
+  CHECK(last >= 0 && last < cus && (!last || 2 * last <= cus), "%d", last);
+  std::vector<int> seen(total + last, 0);
+  const long long blocks = moe::cut_blocks(most, cus);
+  CHECK(blocks % 8 == 0, "%lld", blocks);
+  for (long long b = 0; b < blocks; ++b) {
+    const int i = last ? moe::xcd_item((int)b, total - last, 2 * last) : moe::xcd_item((int)b, total, 0);
+    if (i < 0) continue;
+    CHECK(i < total + last, "block %lld item %d", b, i);
+    if (i < total + last) seen[i]++;
+  }
+  for (int i = 0; i < total + last; ++i) CHECK(seen[i] == 1, "item %d of %d (%d cut): %d", i, total, last, seen[i]);
+}
+
 int main() {
+  for (int total : {1, 7, 255, 256, 257, 300, 383, 384, 385, 511, 513, 1152, 1153, 1800, 4096, 4097, 5000})
+    for (int more : {0, 1, 9, 100}) {
+      cut(total + more, total, 256);
+      cut(total + more, total, 304);
+    }
   for (int E : {1, 2, 16, 64})
     for (int tiles : {1, 3, 7, 8, 9, 100, 1201}) items(E, tiles);
   for (int columns : {64, 128, 256}) {

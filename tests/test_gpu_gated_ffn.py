@@ -283,3 +283,20 @@ def test_gradient_against_differences():
             want, got = (ends[0] - ends[1]) / (2 * h), float(grad.reshape(-1)[at])
             # h^2 / 6 of a third derivative of order 10, 64-bit differences over h, fp32 gradients of order 1
             assert abs(got - want) <= h * h * 10 + 1e-10 / h + 1e-5 * (1 + abs(want)), (name, at, got, want)
+
+
+@pytest.mark.parametrize("op", ["forward", "backward"])
+@pytest.mark.parametrize("T,m,p", [(2900, 8192, 128), (2300, 136, 8200), (1500, 14336, 72)])
+def test_rounds_of_large_tiles(T, m, p, op):
+    """Products of a little more than a round of 256 x 256 tiles: the last round's are cut in two."""
+    log(f"gated {op} T={T} m={m} p={p}")
+    d = make(T, 1, 2, m, p, BF16, seed=12)
+    check_forward(d) if op == "forward" else check_backward(d)
+
+
+def test_weight_gradients_split_over_their_rows():
+    """Few tiles and many rows: the rows are shared and the parts joined, each expert's by its own count."""
+    for dtype in (BF16, F32):
+        d = make(3000, 1, 3, 136, 72, dtype, seed=13)
+        d["offsets"] = torch.tensor([0, 2500, 2500, 2990], dtype=torch.int32, device="cuda")
+        check_backward(d)
