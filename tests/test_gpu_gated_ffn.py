@@ -286,11 +286,14 @@ def test_gradient_against_differences():
 
 
 @pytest.mark.parametrize("op", ["forward", "backward"])
-@pytest.mark.parametrize("T,m,p", [(2900, 8192, 128), (2300, 136, 8200), (1500, 14336, 72)])
-def test_rounds_of_large_tiles(T, m, p, op):
-    """Products of a little more than a round of 256 x 256 tiles: the last round's are cut in two."""
+@pytest.mark.parametrize("T,m,p,split", [(2523, 8192, 64, None), (2400, 64, 8192, None), (2500, 8192, 64, 1000), (2300, 64, 8192, 530)])
+def test_rounds_of_large_tiles(T, m, p, split, op):
+    """Ten row blocks by 32 (or 64) column blocks of 256 x 256 tiles, 1.25 (2.5) rounds of 256: the last round's
+    are cut in two, the halves of a short row block among them."""
     log(f"gated {op} T={T} m={m} p={p}")
-    d = make(T, 1, 2, m, p, BF16, seed=12)
+    d = make(T, 0, 1, m, p, BF16, seed=12) if split is None else make(T, 1, 2, m, p, BF16, seed=12)
+    if split:
+        d["offsets"] = torch.tensor([0, split, T], dtype=torch.int32, device="cuda")
     check_forward(d) if op == "forward" else check_backward(d)
 
 
