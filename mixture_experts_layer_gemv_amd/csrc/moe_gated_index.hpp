@@ -147,9 +147,11 @@ inline GatedChoice choose_gated(bool bf16, int R, long long lines, int stages, i
   }
   // Too few tiles to fill the CUs share their reductions, at least four stages each:
   // one row of 2 experts, 14336 x 4096: 50, unsplit 139 us; 2 rows of 512 x 1024 in fp32: 16 and 45 us.
+  // Joining them takes 5 to 6 us, 15 stages in bf16: XX
   long long splits = slots / n;
   if (splits > stages / 4) splits = stages / 4;
   if (splits > 32) splits = 32;
+  if (stages < (bf16 ? 16 : 10)) splits = 1;
   // Weights that few rows read, too large for the 256 MB last-level cache to hold until
   // the next call: 8 rows each of 16, 1.7 GB: 292 -> 273 us; one of 2, 470 MB: 88 -> 82 us.
   // Small ones, warm: 17.8 -> 21.4 us (1024 x 2048).

@@ -330,13 +330,7 @@ __device__ __forceinline__ int2 expert_rows(const int32_t* offsets, int E, int R
   if (!offsets) return make_int2(0, R);
   const int lane = threadIdx.x & 63;
   auto clamped = [&](int i) { return min(max(i <= E ? offsets[i] : 0, 0), R); };
-  int first = clamped(lane);
-  const int next = clamped(lane + 1);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int p = __shfl_up(first, d, 64);
-    if (lane >= d) first = max(first, p);
-  }
+  const int first = scan_max(clamped(lane)), next = clamped(lane + 1);
   return make_int2(__builtin_amdgcn_readlane(first, e), __builtin_amdgcn_readlane(max(first, next), e));
 }
 

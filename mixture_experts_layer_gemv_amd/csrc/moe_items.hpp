@@ -11,6 +11,30 @@
 
 namespace moe {
 
+// The value that the DPP control CTRL moves to each lane (0 where none does).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_moved(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, true);
+}
+// Over the lanes up to each one (values >= 0): four shifts within rows of 16 lanes,
+// then the rows' last values carried on.
+__device__ __forceinline__ int scan_max(int v) {
+  v = max(v, dpp_moved<0x111, 0xF>(v));  // row_shr:1
+  v = max(v, dpp_moved<0x112, 0xF>(v));
+  v = max(v, dpp_moved<0x114, 0xF>(v));
+  v = max(v, dpp_moved<0x118, 0xF>(v));
+  v = max(v, dpp_moved<0x142, 0xA>(v));         // row_bcast:15 into rows 1 and 3
+  return max(v, dpp_moved<0x143, 0xC>(v));      // row_bcast:31 into rows 2 and 3
+}
+__device__ __forceinline__ int scan_sum(int v) {
+  v += dpp_moved<0x111, 0xF>(v);
+  v += dpp_moved<0x112, 0xF>(v);
+  v += dpp_moved<0x114, 0xF>(v);
+  v += dpp_moved<0x118, 0xF>(v);
+  v += dpp_moved<0x142, 0xA>(v);
+  return v + dpp_moved<0x143, 0xC>(v);
+}
+
 // One (expert, row block, column block) of a launch.
 struct Item {
   int e, mb, nb;   // e < 0: none
@@ -48,21 +72,10 @@ __device__ __forceinline__ Item find_item(const int32_t* offsets, int E, int R, 
   } else {
     const int lane = threadIdx.x & 63;
     auto clamped = [&](int i) { return min(max(i <= E ? offsets[i] : 0, 0), R); };
-    int first = clamped(lane);
-    const int next = clamped(lane + 1);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int p = __shfl_up(first, d, 64);
-      if (lane >= d) first = max(first, p);
-    }
+    const int first = scan_max(clamped(lane)), next = clamped(lane + 1);
     const int end = max(first, next);
     const int items = lane < E ? (end - first + BM - 1) / BM * NBL : 0;
-    int sum = items;  // of the experts up to this one
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int p = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += p;
-    }
+    const int sum = scan_sum(items);  // of the experts up to this one
     const int total = __builtin_amdgcn_readlane(sum, 63);
     L = item_of(L, total);
     if (L < 0 || L >= total) return it;
