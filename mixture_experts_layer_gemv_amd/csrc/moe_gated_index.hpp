@@ -147,11 +147,12 @@ inline GatedChoice choose_gated(bool bf16, int R, long long lines, int stages, i
   }
   // Too few tiles to fill the CUs share their reductions, at least four stages each:
   // one row of 2 experts, 14336 x 4096: 50, unsplit 139 us; 2 rows of 512 x 1024 in fp32: 16 and 45 us.
-  // Joining them takes 5 to 6 us, 15 stages in bf16: XX
+  // Short ones in bf16 do not pay for the join (512 to 1024 wide, one row: 12.1 and 11.3
+  // us; 300 rows each of 4, 640 x 768: 33 and 25 us the pass; one row of 960: 22 and 26).
   long long splits = slots / n;
   if (splits > stages / 4) splits = stages / 4;
   if (splits > 32) splits = 32;
-  if (stages < (bf16 ? 16 : 10)) splits = 1;
+  if (bf16 && stages < (avg > 32 ? 16 : 10)) splits = 1;
   // Weights that few rows read, too large for the 256 MB last-level cache to hold until
   // the next call: 8 rows each of 16, 1.7 GB: 292 -> 273 us; one of 2, 470 MB: 88 -> 82 us.
   // Small ones, warm: 17.8 -> 21.4 us (1024 x 2048).
@@ -167,14 +168,15 @@ struct GradWChoice {
 };
 inline GradWChoice choose_grad_w(bool bf16, int R, int m, int p, int E, int cus) {
   auto tiles = [&](int B) { return 3LL * E * ((m + B - 1) / B) * ((p + B - 1) / B); };
-  // 16 experts, 4096 x 6400: 2.4 ms with 256 x 256 tiles.  Fewer than two a CU are halved:
-  // 207 rows each of 5, 1000 x 712 in fp32: 85 -> 62 us
+  // 16 experts, 4096 x 6400: 2.4 ms with 256 x 256 tiles.  With fewer than two a CU, or
+  // in fp32: 207 rows each of 5, 1000 x 712 in fp32: 85 -> 62 us.  So few that CUs idle share
+  // their rows: 1134 rows of 432 x 560 in fp32: 70 -> 37 us.
   if (bf16 && tiles(256) >= 2 * cus) return {true, 1};
   const int steps = stage_steps(bf16 ? 2 : 4);
   const long long stages = (R / E + steps - 1) / steps;
   long long splits = 2 * cus / tiles(128);
   if (splits > stages / 4) splits = stages / 4;
-  return {false, splits < 2 ? 1 : splits > 32 ? 32 : (int)splits};  // XX
+  return {false, splits < 2 ? 1 : splits > 32 ? 32 : (int)splits};
 }
 
 }  // namespace moe
