@@ -655,7 +655,7 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
  *  dw_router  device fp32 [m][E] or NULL.  db_router  device fp32 [E] or NULL.  Overwritten, with zeros when T is 0.
  *  workspace  with dw_router or db_router: device, 256-byte aligned, at least
  *             moe_route_backward_workspace_size(T, m, E) bytes.  Else NULL.
- *  m a multiple of 8, <= 2^20.
+ *  m a multiple of 8, <= 2^20;  T <= 2^30.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.
  */
 moe_status moe_route_backward_workspace_size(int T, int m, int E, size_t* bytes);

@@ -2183,6 +2183,7 @@ moe_status moe_route_backward(const float* d_topk_w, const int32_t* topk_idx, co
   if (E > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED, "E=%d exceeds %d", E, MOE_MAX_EXPERTS);
   if (moe_status rc = check_value_dtype("x dtype", x_dtype)) return rc;
   if (m > moe::kGatedMaxCols) return fail(MOE_ERR_UNSUPPORTED, "m=%d exceeds %d", m, moe::kGatedMaxCols);
+  if (T > 1 << 30) return fail(MOE_ERR_UNSUPPORTED, "T=%d exceeds 2^30", T);
   const hipStream_t s = as_stream(stream);
   if (T == 0) {  // the sums over no tokens
     if (dw_router) MOE_TRY_HIP(run("fill", s, [&] { return moe::launch_fill_zero(dw_router, (size_t)m * E, s); }));

@@ -125,7 +125,7 @@ def test_route_backward(M):
     for a in [dict(dw=Z), dict(idx=Z), dict(w=Z), dict(x=Z), dict(wr=Z), dict(dl=Z), dict(T=-1), dict(m=0), dict(E=0),
               dict(k=0), dict(k=9), dict(x=FAKE + 8), dict(dxa=FAKE + 8), dict(dx=FAKE + 8), dict(ws=FAKE + 16)]:
         call(bad, **a)
-    for a in [dict(m=12), dict(E=65), dict(dt=2), dict(m=(1 << 20) + 8), dict(T=1 << 30, k=4)]:
+    for a in [dict(m=12), dict(E=65), dict(dt=2), dict(m=(1 << 20) + 8), dict(T=1 << 30, k=4), dict(T=(1 << 30) + 1, k=1)]:
         call(uns, **a)
     for a in [dict(ws=Z), dict(n=need - 1)]:
         call(M.MOE_ERR_WORKSPACE, **a)
