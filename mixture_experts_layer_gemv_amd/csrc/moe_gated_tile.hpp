@@ -14,6 +14,13 @@
 //
 // Reduction steps past the end are copied from a zero block in place of the
 // operands, so nothing that lies there, NaN included, reaches a sum.
+//
+// What bounds it: large products (256 x 256 tiles, two waves per SIMD, 128 x 64 each)
+// the card's power: 16384 x 4096 x 28672 (gate and up) 2.93 ms, 1.31 PFLOP/s, at about
+// 1.65 GHz; over the rows of 8 experts 3.2 ms, over 16 experts' rows 10 to 20 % less, for
+// the rows that their last row blocks lack.  Few rows (32-row tiles) their weights'
+// bytes: 6.0 to 6.4 TB/s from HBM.  fp32 its products (139 TFLOP/s at 4096 x 2048 x 8192)
+// or, in small tiles, the copies into LDS.
 #pragma once
 
 #include <cstddef>
@@ -298,8 +305,8 @@ __device__ __forceinline__ void store_parts(void* p, size_t i, const Vec<T>& f, 
   }
 }
 
-// 1 / (1 + exp(-g)).  In bf16 the fast exponential and reciprocal, good to 2^-21,
-// are well within the output's 2^-9; fp32 takes the exact functions.
+// 1 / (1 + exp(-g)).  In bf16 the fast exponential and reciprocal: within (2 |g| + 8)
+// 2^-24 of the value, where the outputs' half step is 2^-8; fp32 takes the exact functions.
 template <class T>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (T::ES == 2) return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
@@ -583,6 +590,11 @@ void k_gated_rows(const GatedArgs A, int cg, int splits, int cut) {
 }
 
 // ---- weight gradients ----------------------------------------------------------------
+//
+// An expert's rows are the reduction, so each expert has one of its own length; a tile of
+// every matrix of every expert, zeros where it has no rows.  16384 rows of 2 experts, three
+// gradients of 4096 x 6400: 2.09 ms, 1.23 PFLOP/s; of 16 experts 2.43 ms: a fifth of a
+// tile's time goes into its ends.
 
 // PAIR: the hidden operand comes in two parts (GradWProblem::x2, w2), a reduction each.
 template <class T, int TB, int CB, int WT, int WC, int S, bool PAIR>
