@@ -651,7 +651,8 @@ moe_status moe_gated_ffn_backward(const void* dy_perm, const void* x, int dtype,
  *  w_router   device fp32 [m][E] (may be NULL without dx).
  *  dx_add     device [T][m] in x_dtype or NULL: the gradient that reaches x by
  *             another way (the experts' rows, moe_permute_rows_backward).
- *  d_logits   device fp32 [T][E] output.   dx  device [T][m] in x_dtype or NULL; may be dx_add itself.
+ *  d_logits   device fp32 [T][E] output; not d_logits_add, d_topk_w or topk_w.
+ *  dx         device [T][m] in x_dtype or NULL; may be dx_add itself, but with dw_router not x.
  *  dw_router  device fp32 [m][E] or NULL.  db_router  device fp32 [E] or NULL.  Overwritten, with zeros when T is 0.
  *  workspace  with dw_router or db_router: device, 256-byte aligned, at least
  *             moe_route_backward_workspace_size(T, m, E) bytes.  Else NULL.

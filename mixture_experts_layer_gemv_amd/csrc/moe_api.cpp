@@ -2196,6 +2196,10 @@ moe_status moe_route_backward(const float* d_topk_w, const int32_t* topk_idx, co
   if (!all_aligned16({x, dx_add, dx})) return fail(MOE_ERR_INVALID_ARG, "x, dx_add and dx must be 16-byte aligned");
   if (wgrad)
     if (moe_status rc = check_space(workspace, ws_bytes, moe::route_grad_bytes(T, m, E, device_cus()))) return rc;
+  // several workgroups read what one of them writes there
+  if (d_logits == d_logits_add || d_logits == d_topk_w || d_logits == topk_w)
+    return fail(MOE_ERR_INVALID_ARG, "d_logits may not be d_logits_add, d_topk_w or topk_w");
+  if (dw_router && dx && dx == x) return fail(MOE_ERR_INVALID_ARG, "dx may not be x with dw_router");
   moe::RouteGradArgs a{};
   a.dw = d_topk_w;
   a.idx = topk_idx;

@@ -137,6 +137,16 @@ def test_route_backward(M):
         size(4, 60, 8)
 
 
+def test_route_backward_outputs_over_inputs(M):
+    """Rows that several workgroups read while one writes them: every other argument is as it should be."""
+    dw, idx, w, dla, x, wr, dxa, dl, dx, dwr, db, ws = (ctypes.c_void_p(FAKE + (i << 20)) for i in range(12))
+    n = M.moe_route_backward_workspace_size(4, 64, 8)
+    for over in (dla, dw, w):
+        _refused(M, "moe_route_backward", M.MOE_ERR_INVALID_ARG, dw, idx, w, dla, x, 1, wr, dxa, 4, 64, 8, 2, over, dx, dwr, db,
+                 ws, n, Z)
+    _refused(M, "moe_route_backward", M.MOE_ERR_INVALID_ARG, dw, idx, w, dla, x, 1, wr, dxa, 4, 64, 8, 2, dl, x, dwr, db, ws, n, Z)
+
+
 def test_binding_refuses_host_tensors(M):
     import torch
 
