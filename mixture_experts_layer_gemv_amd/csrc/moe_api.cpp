@@ -2002,7 +2002,7 @@ moe_status moe_add_norm_backward(const void* dy, const void* dsum, const void* s
   moe::NormArgs a{};
   a.x = sum;
   a.dy = dy;
-  a.dsum = dsum;
+  a.dsum = dx ? dsum : nullptr;  // it reaches dx alone
   a.gamma = gamma;
   a.out = dx;
   a.mean = const_cast<float*>(mean);
