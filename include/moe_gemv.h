@@ -591,7 +591,8 @@ moe_status moe_add_norm_backward(const void* dy, const void* dsum, const void* s
  *   g = x[t] w_gate[e];  u = x[t] w_up[e];  y_perm[r] = (SiLU(g) * u) w_down[e]
  * The hidden row SiLU(g) * u is rounded to dtype between the projections; bf16
  * ones of up to 32 rows an expert in the mean (rows / min(rows, E)) are kept in two
- * bf16 parts, to 2^-16 of their value.
+ * bf16 parts, to 2^-16 of their value.  Weights that stay as they are, as in serving, are
+ * better packed once (moe_weights_create): moe_expert_ffn takes 2 to 12 % less time on them.
  *  x          device [T][m] in dtype (MOE_F32 or MOE_BF16), as all tensors here.
  *  w_gate, w_up   device [E][m][p].   w_down  device [E][p][m].  (moe_weights_create's w1, w_up, w2.)
  *  offsets    device int32 [E+1] from moe_dispatch, or NULL: E must be 1 and all rows

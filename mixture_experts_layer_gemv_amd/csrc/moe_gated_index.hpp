@@ -39,7 +39,10 @@ MOE_HD inline int transposed_read(int lane, int half, int ks, int t) {
   const int c = 4 * half + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   return k * 128 + 16 * step_place(k, c) + 8 * (lane & 1);
 }
-// fp32: byte of step 8 ks + 4 (lane / 32) + i of column lane % 32 of a group.
+// fp32: byte of step 8 ks + 4 (lane / 32) + i of column lane % 32 of a group.  A read of
+// 4 bytes a lane takes 32 lanes a cycle, 32 columns of one line: no bank twice (333 tokens,
+// top-3 of 12, 1000 x 1720: 5.3 M LDS cycles, which two a read account for, 2 % of them
+// conflicts).
 MOE_HD inline int step_read_f32(int lane, int ks, int i) {
   const int k = 8 * ks + 4 * (lane >> 5) + i;
   return k * 128 + 16 * step_place(k, (lane & 31) >> 2) + 4 * (lane & 3);
@@ -139,14 +142,14 @@ inline GatedChoice choose_gated(bool bf16, int R, long long lines, int stages, i
       const long long tiles = items(BM, 128), most = 2 * cus / tiles, shares = most < stages / 4 ? most : stages / 4;
       return 4 * tiles * (shares > 1 ? shares : 1) >= 6 * cus;
     };
-    // 4096 x 2048 x 8192: 1.01 ms (139 TFLOP/s), 64 x 128 1.10
+    // 4096 x 2048 x 8192: 1.02 ms (135 TFLOP/s), 64 x 128 1.10
     if (avg > 512 && fills(128)) tile = kGated128x128x2, n = items(128, 128), slots = 2 * cus;
     // 207 rows each of 5, 1000 x 712: hidden gradients 35, 128 x 128 47, 32 x 128 41 us (all split)
     else if (avg > 112 && fills(64)) tile = kGated64x128x3, n = items(64, 128), slots = 2 * cus;
     else tile = kGated32x128x2, n = items(32, 128), slots = 4 * cus;
   }
   // Too few tiles to fill the CUs share their reductions, at least four stages each:
-  // one row of 2 experts, 14336 x 4096: 50, unsplit 139 us; 2 rows of 512 x 1024 in fp32: 16 and 45 us.
+  // one row of 2 experts, 14336 x 4096: 52 with the join, unsplit 144 us; 2 rows of 512 x 1024 in fp32: 16 and 45 us.
   // Short ones in bf16 do not pay for the join (512 to 1024 wide, one row: 12.1 and 11.3
   // us; 300 rows each of 4, 640 x 768: 33 and 25 us the pass; one row of 960: 22 and 26).
   long long splits = slots / n;
@@ -155,7 +158,13 @@ inline GatedChoice choose_gated(bool bf16, int R, long long lines, int stages, i
   if (bf16 && stages < (avg > 32 ? 16 : 10)) splits = 1;
   // Weights that few rows read, too large for the 256 MB last-level cache to hold until
   // the next call: 8 rows each of 16, 1.7 GB: 292 -> 273 us; one of 2, 470 MB: 88 -> 82 us.
-  // Small ones, warm: 17.8 -> 21.4 us (1024 x 2048).
+  // Small ones, warm: 17.8 -> 21.4 us (1024 x 2048).  The mean decides, since the host does not
+  // know the counts.  An expert that takes more rows than the mean has several row blocks, which
+  // read its weights at the same time, most of them from the L2: gate and up of 512 rows, 16
+  // experts, 4096 x 6400, a half of the rows for one expert: 417 and, kept, 423 us (even counts
+  // 292 and 307), 2048 rows, 64 experts, 2048 x 1408: 194 and 196 (160 and 170).  Only where one
+  // expert takes all rows, and its weights alone would fit the cache, does it lose: 198 and
+  // 146, 90 and 55 us.
   const bool once = bf16 && avg <= 32 && (long long)experts * lines * stages * 128 >= 128LL << 20;
   return {tile, splits < 2 ? 1 : (int)splits, once};
 }

@@ -19,8 +19,12 @@
 // the card's power: 16384 x 4096 x 28672 (gate and up) 2.93 ms, 1.31 PFLOP/s, at about
 // 1.65 GHz; over the rows of 8 experts 3.2 ms, over 16 experts' rows 10 to 20 % less, for
 // the rows that their last row blocks lack.  Few rows (32-row tiles) their weights'
-// bytes: 6.0 to 6.4 TB/s from HBM.  fp32 its products (139 TFLOP/s at 4096 x 2048 x 8192)
-// or, in small tiles, the copies into LDS.
+// bytes: 6.0 to 6.4 TB/s from HBM.  fp32 its products (135 TFLOP/s at 4096 x 2048 x 8192).
+// fp32 in small tiles no one resource (333 tokens, top-3 of 12, 1000 x 1720: gate and up 90
+// us, down 52): of the CUs' busy cycles the matrix pipe has 73 and 62 %, a sixth of it rows past
+// an expert's last; LDS reads take a tenth of the time, and the waves wait for 15 and 23 %
+// of theirs, for copies that two stages give one stage's time to arrive; and the launch, about
+// one round of tiles, keeps the CUs busy for 83 and 77 % of it.
 #pragma once
 
 #include <cstddef>
@@ -288,8 +292,13 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const Vec<T>& f) {
   *reinterpret_cast<u32x4_t*>(static_cast<char*>(p) + i * T::ES) = r;
 }
 
-// With `low`, what the rounding of f takes off as well, `low` bytes further on: the
-// two parts hold 16 bits of a value.
+// What one product hands to the next is an operand of the bf16 matrix cores there, and so
+// is rounded to bf16.  With `low`, what the rounding of f takes off is stored as well, `low`
+// bytes further on: the two parts hold 16 bits of a value.  They double the products that take
+// them, 6 R m p operations to 8 forwards and 12 to 22 backwards, which is free where the
+// weights' bytes bound the time (gated_pairs) and would cost their share where the products
+// do; there a hidden value keeps bf16's 8 bits, as in the packed experts, and an output is off
+// by 0.0024 of its size in place of 0.0017, which one rounding leaves.
 template <class T>
 __device__ __forceinline__ void store_parts(void* p, size_t i, const Vec<T>& f, ptrdiff_t low) {
   store_vec<T>(p, i, f);
