@@ -298,7 +298,7 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const Vec<T>& f) {
 // them, 6 R m p operations to 8 forwards and 12 to 22 backwards, which is free where the
 // weights' bytes bound the time (gated_pairs) and would cost their share where the products
 // do; there a hidden value keeps bf16's 8 bits, as in the packed experts, and an output is off
-// by 0.0024 of its size in place of 0.0017, which one rounding leaves.
+// by 0.0023 of its size in place of 0.0017, which one rounding leaves.
 template <class T>
 __device__ __forceinline__ void store_parts(void* p, size_t i, const Vec<T>& f, ptrdiff_t low) {
   store_vec<T>(p, i, f);
